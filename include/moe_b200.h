@@ -71,7 +71,8 @@ typedef enum {
 typedef enum {
   MOE_ACT_SILU = 0, /* SwiGLU: silu(g) = g / (1 + exp(-g)) */
   MOE_ACT_GELU = 1, /* GeGLU:  gelu(g) = g/2 * (1 + erf(g / sqrt 2)), the exact form */
-  MOE_ACT_RELU = 2  /* ReGLU:  relu(g) = max(g, 0) */
+  MOE_ACT_RELU = 2, /* ReGLU:  relu(g) = max(g, 0) */
+  MOE_ACT_NONE = -1 /* the identity: moe_linear and moe_linear_backward only */
 } moe_activation;
 
 /* Problem shape. T tokens, hidden size H, expert intermediate size I,
@@ -263,6 +264,115 @@ moe_status moe_forward_noalloc(const moe_shape* shape, const void* x, const int3
  * Like the forward's scratch, the word is shared by every call on the device:
  * read it after the call it should describe and before the next one. */
 moe_status moe_forward_noalloc_status(void* stream);
+
+/* ------------------------------------------------------------------------
+ * The dense operators around the routed experts: what every token of a
+ * mixture-of-experts block passes besides the router and its chosen experts.
+ * All are bf16 with fp32 sums, take contiguous row-major tensors, run on
+ * `stream`, allocate nothing and are deterministic. T = 0 is valid (outputs
+ * with no token rows are untouched, weight gradients are set to zero).
+ *
+ * Requirements, else MOE_ERR_INVALID_ARG: sizes other than T positive
+ * multiples of 8 and at most 2^20 (H of the norm at most 65536); bf16 and fp32
+ * matrices 16-byte aligned, rstd and scales 4-byte aligned, workspaces 256-byte
+ * aligned; no output overlaps an input or another output, except where an
+ * entry point allows the two to be the same buffer. MOE_ERR_WORKSPACE for a
+ * workspace smaller than the matching ..._workspace_size(); MOE_ERR_CUDA for a
+ * failed launch. A bounded device wait that gives up (never in normal
+ * operation) writes NaN into the outputs it did not compute. Calls that share
+ * a workspace must not overlap in time.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * moe_rms_norm -- root-mean-square norm with the residual's addition:
+ *   s = bf16(x + residual)          (s = x when residual is NULL)
+ *   r[t] = (mean_i s[t,i]^2 + eps)^(-1/2),   y[t,i] = s[t,i] r[t] weight[i]
+ *   x, residual   [T, H] bf16; residual may be NULL
+ *   weight        [H] bf16
+ *   eps           > 0, finite
+ *   y             [T, H] bf16 out, or NULL when only codes are wanted
+ *   residual_out  [T, H] bf16 out: s, or NULL
+ *   codes, scales e4m3 [T, H] and fp32 [T, H/128] out, or both NULL: the fp32 y
+ *                 in the form of the FP8 experts' activations, per 128 columns
+ *                 scale = amax/448 (1 for an all-zero group), code =
+ *                 e4m3(y/scale). H must be a multiple of 128.
+ *   rstd          [T] fp32 out: r, for moe_rms_norm_backward; or NULL
+ * y and residual_out may each be x or residual (the same buffer, not each other).
+ */
+moe_status moe_rms_norm(const void* x, const void* residual, const void* weight, int32_t T, int32_t H, float eps,
+                        void* y, void* residual_out, uint8_t* codes, float* scales, float* rstd, void* stream);
+
+/* Bytes of workspace moe_rms_norm_backward needs (host-only; 0 for invalid sizes). */
+size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H);
+
+/*
+ * moe_rms_norm_backward -- gradients of moe_rms_norm from dy [T, H] (at y) and
+ * dresidual [T, H] (at residual_out; NULL for none), with s, weight and rstd as
+ * the forward had them:
+ *   dx = r (w dy - s r^2 mean(w dy s)) + dresidual     [T, H] bf16 out: the
+ *        gradient of x and, the same values, of residual
+ *   dw = sum_t dy s r                                  [H] bf16 out
+ * dx may be dy or dresidual.
+ */
+moe_status moe_rms_norm_backward(const void* dy, const void* s, const void* weight, const float* rstd,
+                                 const void* dresidual, int32_t T, int32_t H, void* dx, void* dw, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * moe_gated_ffn -- both projections of a gated MLP, the activation and the
+ * product in one kernel, for every token (a shared expert, or a dense layer):
+ *   h = act(x Wg^T) * (x Wu^T)
+ *   x          [T, H] bf16
+ *   w_gate_up  [2I, H] bf16: rows 0..I-1 the gate, I..2I-1 the up projection
+ *              (one expert's layout in moe_forward)
+ *   act        MOE_ACT_SILU, MOE_ACT_GELU or MOE_ACT_RELU
+ *   h          [T, I] bf16 out
+ *   gu         [T, 2I] fp32 out: x Wg^T, x Wu^T for the backward pass; or NULL
+ */
+moe_status moe_gated_ffn(const void* x, const void* w_gate_up, int32_t T, int32_t H, int32_t I, int32_t act, void* h,
+                         float* gu, void* stream);
+
+/* Bytes of workspace moe_gated_ffn_backward needs (host-only; 0 for invalid sizes). */
+size_t moe_gated_ffn_backward_workspace_size(int32_t T, int32_t I);
+
+/*
+ * moe_gated_ffn_backward -- gradients of moe_gated_ffn from dh [T, I], with
+ * x, w_gate_up and the gu that the forward kept:
+ *   dg = dh u act'(g), du = dh act(g)    (rounded to bf16 for the products)
+ *   dx = dg Wg + du Wu                   [T, H] bf16 out, or NULL
+ *   dw = [dg, du]^T x                    [2I, H] bf16 out, or NULL
+ */
+moe_status moe_gated_ffn_backward(const void* dh, const void* x, const void* w_gate_up, const float* gu, int32_t T,
+                                  int32_t H, int32_t I, int32_t act, void* dx, void* dw, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * moe_linear -- a projection with bias, activation and residual in its
+ * epilogue (a shared expert's down projection, added to the routed sum):
+ *   z = x W^T + bias,   y = act(z) + residual      (fp32, rounded once)
+ *   x [T, K], w [N, K] bf16; bias [N] bf16 or NULL; residual [T, N] bf16 or NULL
+ *   act   MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU or MOE_ACT_RELU
+ *   y     [T, N] bf16 out; may be residual
+ *   z     [T, N] fp32 out for the backward pass of an activation; or NULL
+ */
+moe_status moe_linear(const void* x, const void* w, const void* bias, const void* residual, int32_t T, int32_t K,
+                      int32_t N, int32_t act, void* y, float* z, void* stream);
+
+/* Bytes of workspace moe_linear_backward needs (host-only; 0 for invalid
+ * sizes); has_db: whether db is wanted. */
+size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t act, int32_t has_db);
+
+/*
+ * moe_linear_backward -- gradients of moe_linear from dy [T, N]:
+ *   dz = dy act'(z)     (rounded to bf16 for the products; dy itself without an activation)
+ *   dx = dz W           [T, K] bf16 out, or NULL
+ *   dw = dz^T x         [N, K] bf16 out, or NULL
+ *   db = sum_t dz       [N] bf16 out, or NULL (summed from the fp32 dz)
+ * The residual's gradient is dy. z may be NULL with MOE_ACT_NONE.
+ */
+moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const float* z, int32_t T, int32_t K,
+                               int32_t N, int32_t act, void* dx, void* dw, void* db, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(moe_status status);

@@ -29,7 +29,10 @@ ACT = {"silu": 0, "gelu": 1, "relu": 2}
 PATH_NAMES = {v: k for k, v in PATH.items()}
 EXPORTS = ["moe_route", "moe_workspace_size", "moe_forward", "moe_forward_timed", "moe_workspace_query",
            "moe_read_device_status", "moe_status_string", "moe_version", "moe_forward_noalloc",
-           "moe_set_test_hooks", "moe_router", "moe_forward_noalloc_status"]
+           "moe_set_test_hooks", "moe_router", "moe_forward_noalloc_status",
+           "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_size",
+           "moe_gated_ffn", "moe_gated_ffn_backward", "moe_gated_ffn_backward_workspace_size",
+           "moe_linear", "moe_linear_backward", "moe_linear_backward_workspace_size"]
 
 
 class MoeError(RuntimeError):
@@ -84,6 +87,20 @@ def lib() -> ctypes.CDLL:
         L.moe_router.restype = i32
         L.moe_set_test_hooks.argtypes = [i32, ctypes.c_uint64]
         L.moe_set_test_hooks.restype = i32
+        f32 = ctypes.c_float
+        for name, args in (
+                ("moe_rms_norm", [vp, vp, vp, i32, i32, f32, vp, vp, vp, vp, vp, vp]),
+                ("moe_rms_norm_backward", [vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]),
+                ("moe_gated_ffn", [vp, vp, i32, i32, i32, i32, vp, vp, vp]),
+                ("moe_gated_ffn_backward", [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
+                ("moe_linear", [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]),
+                ("moe_linear_backward", [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = i32
+        for name, n in (("moe_rms_norm_backward_workspace_size", 2), ("moe_gated_ffn_backward_workspace_size", 2),
+                        ("moe_linear_backward_workspace_size", 4)):
+            getattr(L, name).argtypes = [i32] * n
+            getattr(L, name).restype = sz
         L.moe_version.argtypes = []
         L.moe_version.restype = i32
         _lib = L
@@ -312,6 +329,10 @@ def set_test_hooks(stall_gate_up_loads: bool = False, wait_limit_ns: int = 0) ->
     _check(lib().moe_set_test_hooks(int(bool(stall_gate_up_loads)), int(wait_limit_ns)), "moe_set_test_hooks")
 
 
+from .dense import (RMSNormOutput, gated_ffn, gated_ffn_backward, linear, linear_backward,  # noqa: E402
+                    rms_norm, rms_norm_backward)
+
+
 class MoELayer:
     """A routed MoE layer whose expert weights live on the GPU: ``layer(x, logits)``
     runs moe_route then moe_forward and returns bf16 [T,H]. The workspace is
@@ -446,4 +467,5 @@ class MoEPipeline:
 
 __all__ = ["lib", "route", "forward", "forward_noalloc", "noalloc_device_status", "MoEGraph", "MoEPipeline", "workspace_size", "workspace_layout", "alloc_workspace",
            "read_device_status", "set_test_hooks", "router", "make_shape", "MoELayer", "MoeError", "MoeShape", "EXPORTS", "STATUS",
-           "status_string", "PATH", "WDTYPE", "ACT"]
+           "status_string", "PATH", "WDTYPE", "ACT", "rms_norm", "rms_norm_backward", "RMSNormOutput", "gated_ffn",
+           "gated_ffn_backward", "linear", "linear_backward"]

@@ -1,0 +1,540 @@
+// Dense GEMM on CTA pairs or single CTAs: tcgen05 tiles of one matrix for the
+// whole batch (no routing), with the epilogues a shared expert needs.
+//
+//   linear:  out[m, n] = bf16(act(sum_k A[m,k] B[n,k] + bias[n]) + residual[m, n])
+//   gated:   out[m, n] = bf16(act(sum_k A[m,k] B[n,k]) * sum_k A[m,k] B[N+n,k])
+// optionally keeping the fp32 pre-activations (linear z[m,n]; gated g and u)
+// for the backward pass. The products of the backward pass are linear ones
+// with other operand orders: dx = dz W reads W as an MN-major B, and
+// dW = dz^T x reads both operands MN-major, so nothing is transposed in memory.
+//
+// Tiles: a pair (cta_group::2) computes 256 x kBN, a single CTA 128 x kBN; the
+// gated form takes kBN/2 gate and kBN/2 up rows of B for one tile (in a pair
+// the leader stages the gate rows, the peer the up rows), so one TMEM lane
+// holds both halves of each of its outputs. K runs in steps of 64 through a
+// TMA ring of 128-byte-swizzled tiles; two accumulator buffers in TMEM let the
+// epilogue of a tile overlap the next tile's MMAs. Ragged edges are TMA's:
+// loads fill zeros past the tensor, stores clip.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 2..9 epilogue (two per TMEM lane
+// quadrant, each half of the tile's columns, 32 at a time through two 2 KB
+// staging buffers and TMA tile stores). Accumulation is fp32 in TMEM; bias,
+// activation and residual are applied in fp32 before the one rounding.
+//
+// Every wait is bounded; a CTA whose wait gave up writes NaN into its tiles.
+#include <algorithm>
+
+#include "dense_core.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 64;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBox = 32 * 64;  // a staging buffer: 32 rows of 64 bytes
+constexpr int kStaging = kEpiWarps * 2 * kBox;
+constexpr int kGroupM = 8;  // row blocks that are walked together along the columns (their A and B tiles meet in L2)
+
+struct GemmParams {
+  int M, N;  // of the output
+  int num_kb, m_tiles, n_tiles;
+  int act, save, stall;
+  int up_row;  // gated: first up row of B
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* out;
+  unsigned long long timeout_ns;
+};
+
+template <bool kPair, int kBN>
+struct Tile {
+  static constexpr int kCtas = kPair ? 2 : 1;
+  static constexpr int kBRows = kBN / kCtas;  // rows of B in one CTA
+  static constexpr int kA = kTileM * kBK * 2;
+  static constexpr int kB = kBRows * kBK * 2;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = 196608 / kStage < 8 ? 196608 / kStage : 8;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kStaging + (2 * kStages + 5) * 8 + 16;
+};
+
+__device__ __forceinline__ void tile_coord(int tile, int m_tiles, int n_tiles, int& m, int& n) {
+  const int per = kGroupM * n_tiles;
+  const int g = tile / per;
+  const int gm = min(kGroupM, m_tiles - g * kGroupM);
+  const int r = tile - g * per;
+  n = r / gm;
+  m = g * kGroupM + (r - n * gm);
+}
+
+// acc = act(acc) for the 32 columns in registers
+template <int kAct>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = act_t<kAct>(v[i]);
+}
+template <int kAct>
+__device__ __forceinline__ void gate32(float (&g)[32], const float (&u)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) g[i] = gated_act_t<kAct>(g[i], u[i]);
+}
+
+// The warp's two staging buffers and the TMA stores out of them.
+struct Stager {
+  uint8_t* base;
+  int buf;
+  int lane;
+  // a buffer whose last store has been read out
+  __device__ __forceinline__ uint32_t take() {
+    if (lane == 0) bulk_wait_group_read<1>();
+    __syncwarp();
+    return smem_u32(base + buf * kBox);
+  }
+  __device__ __forceinline__ void store(const CUtensorMap* map, int x, int y, bool in) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (in) tma_store_2d(map, base + buf * kBox, x, y);
+      bulk_commit_group();
+    }
+    buf ^= 1;
+  }
+  // 32 fp32 columns as two boxes of 16
+  __device__ __forceinline__ void store_f32(const CUtensorMap* map, const float (&v)[32], int x, int y, int N,
+                                            bool in) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sb = take();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st_shared_v4(sb + sw64_offset(lane, i), __float_as_uint(v[16 * h + 4 * i]),
+                     __float_as_uint(v[16 * h + 4 * i + 1]), __float_as_uint(v[16 * h + 4 * i + 2]),
+                     __float_as_uint(v[16 * h + 4 * i + 3]));
+      store(map, x + 16 * h, y, in && x + 16 * h < N);
+    }
+  }
+  __device__ __forceinline__ void store_bf16(const CUtensorMap* map, const float (&v)[32], int x, int y, bool in) {
+    const uint32_t sb = take();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      st_shared_v4(sb + sw64_offset(lane, i), pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                   pack_bf16x2(v[8 * i + 2], v[8 * i + 3]), pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                   pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    store(map, x, y, in);
+  }
+};
+
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32(addr, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <bool kPair, int kBN, bool kAmn, bool kBmn, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS0,
+                      const __grid_constant__ CUtensorMap tmS1, const GemmParams p) {
+  using TL = Tile<kPair, kBN>;
+  constexpr int kStages = TL::kStages;
+  constexpr int kOutN = kGated ? kBN / 2 : kBN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kStages * TL::kA;
+  uint8_t* sY = sB + kStages * TL::kB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sY + kStaging);  // used in the leader
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;  // [2]
+  uint64_t* tempty = tfull + 2;       // [2] used in the leader
+  uint64_t* drain = tempty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_status = reinterpret_cast<int*>(s_tmem + 2);  // the bounded waits record here; NaN outputs tell the caller
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kEpiWarps * TL::kCtas);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    *s_status = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+    prefetch_tensormap(&tmY);
+  }
+  if (warp == 1) {
+    if (kPair) {
+      tmem_alloc_pair(s_tmem, 2 * kBN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(s_tmem, 2 * kBN);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (kPair) cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
+  pdl_trigger();
+  const int total = p.m_tiles * p.n_tiles;
+  const int worker = blockIdx.x / TL::kCtas, nworkers = gridDim.x / TL::kCtas;
+
+  if (warp == 0) {
+    if (lane == 0 && !p.stall) {
+      // ---------------- TMA producer ----------------
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = worker; ok && tile < total; tile += nworkers) {
+        int mt, nt;
+        tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
+        const int m0 = (mt * TL::kCtas + rank) * kTileM;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&full[stage], TL::kCtas * TL::kStage);
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+            if (kPair)
+              tma_load_2d_pair(dst, map, leader_addr(&full[stage]), x, y);
+            else
+              tma_load_2d(dst, map, &full[stage], x, y);
+          };
+          uint8_t* a = sA + stage * TL::kA;
+          uint8_t* b = sB + stage * TL::kB;
+          const int k0 = kb * kBK;
+          if (kAmn) {
+            load(a, &tmA, m0, k0);
+            load(a + 8192, &tmA, m0 + 64, k0);
+          } else {
+            load(a, &tmA, k0, m0);
+          }
+          if (kGated) {
+            if (kPair) {
+              load(b, &tmB, k0, nt * kOutN + rank * p.up_row);
+            } else {
+              load(b, &tmB, k0, nt * kOutN);
+              load(b + TL::kB / 2, &tmB, k0, nt * kOutN + p.up_row);
+            }
+          } else if (kBmn) {
+#pragma unroll
+            for (int j = 0; j < TL::kBRows / 64; ++j)
+              load(b + j * 8192, &tmB, nt * kBN + rank * TL::kBRows + 64 * j, k0);
+          } else {
+            load(b, &tmB, k0, nt * kBN + rank * TL::kBRows);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok && leader) {
+        // let the copies already issued (of both CTAs) land before the CTA can exit
+        for (int i = 0; i < kStages; ++i) {
+          if (--stage < 0) {
+            stage = kStages - 1;
+            ph ^= 1;
+          }
+          int never = 0;
+          mbar_wait_bounded(&full[stage], ph, &never, s_status, 1000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idesc = idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, kAmn, kBmn);
+      int stage = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int tile = worker; ok && tile < total; tile += nworkers) {
+        if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, s_abort, s_status, p.timeout_ns)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait_bounded(&full[stage], ph, s_abort, s_status, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + stage * TL::kA);
+          const uint32_t b0 = smem_u32(sB + stage * TL::kB);
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) {
+            const uint64_t da = kAmn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32);
+            const uint64_t db = kBmn ? sdesc_mnmajor_sw128(b0 + k * 2048) : sdesc_kmajor_sw128(b0 + k * 32);
+            if (kPair)
+              umma_bf16_pair(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+            else
+              umma_bf16(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          if (kPair)
+            umma_commit_pair_mc(&empty[stage], 0x3);
+          else
+            umma_commit(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (kPair)
+          umma_commit_pair_mc(&tfull[acc], 0x3);
+        else
+          umma_commit(&tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) aph ^= 1;
+      }
+      if (kPair)
+        umma_commit_pair(drain);
+      else
+        umma_commit(drain);
+      int never = 0;
+      mbar_wait_bounded(drain, 0, &never, s_status, p.timeout_ns);
+    }
+  } else {
+    // ---------------- epilogue (own 128 rows) ----------------
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    constexpr int kCols = kOutN / 2;  // output columns of this warp
+    Stager st{sY + (warp - 2) * 2 * kBox, 0, lane};
+    int acc = 0;
+    uint32_t aph = 0;
+    int tile = worker;
+    for (; tile < total; tile += nworkers) {
+      int mt, nt;
+      tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
+      const int y0 = (mt * TL::kCtas + rank) * kTileM + quad * 32;
+      const int x0 = nt * kOutN + half * kCols;
+      const bool got = mbar_wait_bounded(&tfull[acc], aph, s_abort, s_status, p.timeout_ns);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                          static_cast<uint32_t>(acc * kBN + half * kCols);
+      const bool rows = y0 < p.M;
+      const bool mine = y0 + lane < p.M;
+      const __nv_bfloat16* res =
+          p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * p.N : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 32) {
+        const int x = x0 + c;
+        float v[32];
+        if (kGated) {
+          float u[32];
+          tmem_load32(tb + c, v);
+          tmem_load32(tb + kOutN + c, u);
+          if (p.save) {
+            st.store_f32(&tmS0, v, x, y0, p.N, rows);
+            st.store_f32(&tmS1, u, x, y0, p.N, rows);
+          }
+          if (p.act == MOE_ACT_SILU)
+            gate32<MOE_ACT_SILU>(v, u);
+          else if (p.act == MOE_ACT_GELU)
+            gate32<MOE_ACT_GELU>(v, u);
+          else
+            gate32<MOE_ACT_RELU>(v, u);
+        } else {
+          uint4 rv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            rv[i] = res != nullptr && x + 8 * i < p.N ? *reinterpret_cast<const uint4*>(res + x + 8 * i)
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+          tmem_load32(tb + c, v);
+          if (p.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (x + 8 * i >= p.N) continue;
+              const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + x + 8 * i));
+              const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[8 * i + 2 * q] += bf16_lo(w[q]);
+                v[8 * i + 2 * q + 1] += bf16_hi(w[q]);
+              }
+            }
+          }
+          if (p.save) st.store_f32(&tmS0, v, x, y0, p.N, rows);
+          if (p.act == MOE_ACT_SILU)
+            act32<MOE_ACT_SILU>(v);
+          else if (p.act == MOE_ACT_GELU)
+            act32<MOE_ACT_GELU>(v);
+          else if (p.act == MOE_ACT_RELU)
+            act32<MOE_ACT_RELU>(v);
+          if (p.residual != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[8 * i + 2 * q] += bf16_lo(w[q]);
+                v[8 * i + 2 * q + 1] += bf16_hi(w[q]);
+              }
+            }
+          }
+        }
+        st.store_bf16(&tmY, v, x, y0, rows && x < p.N);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair)
+          mbar_arrive_cluster(leader_addr(&tempty[acc]));
+        else
+          mbar_arrive(&tempty[acc]);
+      }
+      acc ^= 1;
+      if (acc == 0) aph ^= 1;
+    }
+    // a wait gave up (never in normal operation): mark what this warp did not compute
+    for (; tile < total; tile += nworkers) {
+      int mt, nt;
+      tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
+      const int y = (mt * TL::kCtas + rank) * kTileM + quad * 32 + lane;
+      const int x0 = nt * kOutN + half * kCols;
+      if (y < p.M)
+        for (int x = x0; x < min(x0 + kCols, p.N); ++x)
+          p.out[static_cast<size_t>(y) * p.N + x] = __ushort_as_bfloat16(0x7FC0);
+    }
+    if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
+  }
+
+  __syncthreads();
+  if (kPair) cluster_sync();  // neither CTA frees TMEM while the pair still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    if (kPair)
+      tmem_dealloc_pair(tmem_base, 2 * kBN);
+    else
+      tmem_dealloc(tmem_base, 2 * kBN);
+  }
+}
+
+template <bool kPair, int kBN, bool kAmn, bool kBmn, bool kGated>
+cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
+  using TL = Tile<kPair, kBN>;
+  constexpr int kOutN = kGated ? kBN / 2 : kBN;
+  GemmParams p{};
+  p.M = g.M;
+  p.N = g.N;
+  p.num_kb = (g.K + kBK - 1) / kBK;
+  p.m_tiles = (g.M + kTileM * TL::kCtas - 1) / (kTileM * TL::kCtas);
+  p.n_tiles = (g.N + kOutN - 1) / kOutN;
+  if (static_cast<long long>(p.m_tiles) * p.n_tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+  p.act = g.act;
+  p.save = g.save0 != nullptr;
+  p.stall = stall_gate_up_loads();
+  p.up_row = g.N;
+  p.bias = static_cast<const __nv_bfloat16*>(g.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(g.residual);
+  p.out = static_cast<__nv_bfloat16*>(g.out);
+  p.timeout_ns = wait_limit_ns();
+
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const uint64_t b_rows = kGated ? 2 * static_cast<uint64_t>(g.N) : g.N;
+  CUtensorMap tmA, tmB, tmY, tmS0, tmS1;
+  bool ok = kAmn ? encode_tensor_map_2d(&tmA, bf16, 2, g.a, g.M, g.K, 64, kBK)
+                 : encode_tensor_map_2d(&tmA, bf16, 2, g.a, g.K, g.M, kBK, kTileM);
+  ok = ok && (kBmn ? encode_tensor_map_2d(&tmB, bf16, 2, g.b, g.N, g.K, 64, kBK)
+                   : encode_tensor_map_2d(&tmB, bf16, 2, g.b, g.K, b_rows, kBK,
+                                          kGated ? kOutN : TL::kBRows));
+  ok = ok && encode_tensor_map_2d(&tmY, bf16, 2, g.out, g.N, g.M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!ok) return cudaErrorInvalidValue;
+  tmS0 = tmS1 = tmY;
+  if (p.save) {
+    const uint64_t ld = kGated ? 2 * static_cast<uint64_t>(g.N) : g.N;
+    if (!encode_tensor_map_2d_ld(&tmS0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.save0, g.N, g.M, ld, 16, 32,
+                                 CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+    if (kGated && !encode_tensor_map_2d_ld(&tmS1, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.save0 + g.N, g.N, g.M, ld, 16,
+                                           32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
+
+  auto kernel = dense_gemm_kernel<kPair, kBN, kAmn, kBmn, kGated>;
+  static unsigned long long done = 0;
+  cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
+  if (err != cudaSuccess) return err;
+  int workers = std::min(num_sms / TL::kCtas, p.m_tiles * p.n_tiles);
+  if (kPair) {
+    // every pair of the persistent grid must be resident at once
+    const int maxc = max_active_clusters(reinterpret_cast<const void*>(kernel), 2, kThreads, TL::kSmem);
+    if (maxc > 0) workers = std::min(workers, maxc);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1, workers) * TL::kCtas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = TL::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = TL::kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmY, tmS0, tmS1, p);
+}
+
+// Tile choice: the shape with the least estimated time, waves x (K steps x
+// cycles a step + tile overhead).
+template <bool kAmn, bool kBmn, bool kGated>
+cudaError_t launch_order(const DenseGemm& g, int num_sms, cudaStream_t st) {
+  const long long kb = (g.K + kBK - 1) / kBK;
+  auto cost = [&](int rows, int cols, int slots, int per_step) {
+    const int outn = kGated ? cols / 2 : cols;
+    const long long tiles = ((g.M + rows - 1ll) / rows) * ((g.N + outn - 1ll) / outn);
+    return ((tiles + slots - 1) / slots) * (kb * per_step + 1000);
+  };
+  const long long c[4] = {cost(256, 256, num_sms / 2, 560), cost(256, 128, num_sms / 2, 340),
+                          cost(128, 256, num_sms, 640), cost(128, 128, num_sms, 400)};
+  int best = 0;
+  for (int i = 1; i < 4; ++i)
+    if (c[i] < c[best]) best = i;
+  if (g.force >= 0) best = g.force;
+  switch (best) {
+    case 0:
+      return launch_t<true, 256, kAmn, kBmn, kGated>(g, num_sms, st);
+    case 1:
+      return launch_t<true, 128, kAmn, kBmn, kGated>(g, num_sms, st);
+    case 2:
+      return launch_t<false, 256, kAmn, kBmn, kGated>(g, num_sms, st);
+    default:
+      return launch_t<false, 128, kAmn, kBmn, kGated>(g, num_sms, st);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st) {
+  switch (g.order) {
+    case kGatedNT:
+      return launch_order<false, false, true>(g, num_sms, st);
+    case kLinearNT:
+      return launch_order<false, false, false>(g, num_sms, st);
+    case kLinearNN:
+      return launch_order<false, true, false>(g, num_sms, st);
+    default:
+      return launch_order<true, true, false>(g, num_sms, st);
+  }
+}
+
+}  // namespace moe

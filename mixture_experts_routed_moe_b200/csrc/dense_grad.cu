@@ -1,0 +1,137 @@
+// Elementwise halves of the dense operators' backward passes: the gradients
+// at the pre-activations, from the fp32 pre-activations the forward kept.
+//
+//   gated:  dg = dh u act'(g),  du = dh act(g)        -> bf16 [T, 2I]
+//   linear: dz = dy act'(z)                           -> bf16 [T, N]
+//           db = sum_t dz                             (from the fp32 dz)
+//
+// HBM-bound: 16-byte loads and stores, each element once. dg, du and dz are
+// rounded to bf16 because they are the tensor cores' operands of the products
+// that follow; the column sums are fp32 in a fixed order.
+#include <algorithm>
+
+#include "dense_core.cuh"
+
+namespace moe {
+namespace {
+
+__global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict__ gu,
+                                                         const __nv_bfloat16* __restrict__ dh,
+                                                         __nv_bfloat16* __restrict__ dgu, long long T, int I, int act) {
+  pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
+  pdl_trigger();
+  const int nv = I / 8;
+  const long long n = T * nv;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+    const long long t = i / nv;
+    const int c = static_cast<int>(i - t * nv) * 8;
+    const float4* gp = reinterpret_cast<const float4*>(gu + 2 * t * I + c);
+    const float4* up = reinterpret_cast<const float4*>(gu + 2 * t * I + I + c);
+    const float4 g0 = gp[0], g1 = gp[1], u0 = up[0], u1 = up[1];
+    const uint4 d = *reinterpret_cast<const uint4*>(dh + t * I + c);
+    const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+    const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+    uint32_t og[4], ou[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float f0, s0, f1, s1;
+      act_and_slope(act, g[2 * q], f0, s0);
+      act_and_slope(act, g[2 * q + 1], f1, s1);
+      const float a = bf16_lo(dw[q]), b = bf16_hi(dw[q]);
+      og[q] = pack_bf16x2(a * u[2 * q] * s0, b * u[2 * q + 1] * s1);
+      ou[q] = pack_bf16x2(a * f0, b * f1);
+    }
+    *reinterpret_cast<uint4*>(dgu + 2 * t * I + c) = make_uint4(og[0], og[1], og[2], og[3]);
+    *reinterpret_cast<uint4*>(dgu + 2 * t * I + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  }
+}
+
+// Block (x, y): 256 columns (8 per lane of a warp), rows y, y + 8, ... by its
+// eight warps within the row range of blockIdx.y; dz written, the fp32 column
+// sums of the range added over the warps in order and left in partial[y].
+__global__ void __launch_bounds__(256) linear_grad_kernel(const float* __restrict__ z,
+                                                          const __nv_bfloat16* __restrict__ dy,
+                                                          __nv_bfloat16* __restrict__ dz, float* __restrict__ partial,
+                                                          long long T, int N, int act) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_sum[8][257];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + lane * 8;
+  const long long t0 = blockIdx.y * T / gridDim.y, t1 = (blockIdx.y + 1) * T / gridDim.y;
+  float sum[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) sum[q] = 0.f;
+  if (c < N) {
+#pragma unroll 2
+    for (long long t = t0 + warp; t < t1; t += 8) {
+      const size_t at = static_cast<size_t>(t) * N + c;
+      const uint4 d = *reinterpret_cast<const uint4*>(dy + at);
+      const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[2 * q] = bf16_lo(dw[q]);
+        v[2 * q + 1] = bf16_hi(dw[q]);
+      }
+      if (act != kActNone) {
+        const float4* zp = reinterpret_cast<const float4*>(z + at);
+        const float4 z0 = zp[0], z1 = zp[1];
+        const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float f, s;
+          act_and_slope(act, zz[q], f, s);
+          v[q] *= s;
+        }
+        *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] += v[q];
+    }
+  }
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s_sum[warp][lane * 8 + q] = sum[q];
+  __syncthreads();
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col < N) {
+    float t = s_sum[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t += s_sum[w][threadIdx.x];
+    partial[static_cast<size_t>(blockIdx.y) * N + col] = t;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T, int I, int act, int num_sms,
+                              cudaStream_t st) {
+  const long long n = static_cast<long long>(T) * (I / 8);
+  const long long blocks = std::min<long long>((n + 255) / 256, static_cast<long long>(num_sms) * 8);
+  return launch_pdl(gated_grad_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, gu,
+                    static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dgu),
+                    static_cast<long long>(T), I, act);
+}
+
+int linear_grad_rows(int T, int N) {
+  // row ranges: enough blocks for the device, at least 32 rows each
+  const int cols = (N + 255) / 256;
+  return std::max(1, std::min((T + 31) / 32, (1184 + cols - 1) / cols));
+}
+
+cudaError_t launch_linear_grad(const float* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
+                               int act, cudaStream_t st) {
+  const int rows = linear_grad_rows(T, N);
+  cudaError_t err = launch_pdl(linear_grad_kernel, dim3(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(rows)),
+                               dim3(256), 0, st, z, static_cast<const __nv_bfloat16*>(dy),
+                               static_cast<__nv_bfloat16*>(dz), db != nullptr ? partial : static_cast<float*>(nullptr),
+                               static_cast<long long>(T), N, act);
+  if (err != cudaSuccess || db == nullptr) return err;
+  return launch_column_sum(partial, rows, N, db, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,327 @@
+// The dense GEMMs for few tokens: the weight rows are the MMA's M, the tokens
+// its N, and K is split over a cluster, so that a decode batch streams the
+// weights at HBM rate from every SM instead of filling a few token tiles.
+//
+//   linear:  out[t, n] = bf16(act(sum_k W[n,k] X[t,k] + bias[n]) + residual[t, n])
+//   gated:   out[t, n] = bf16(act(sum_k W[n,k] X[t,k]) * sum_k W[N+n,k] X[t,k])
+//
+// with W read K-major, or MN-major (linear only: dx = dz W of the backward
+// pass, where W^T's rows are the outputs). A unit is 128 weight rows (gated: 64
+// gate rows and the 64 up rows that belong to them); a cluster of C CTAs owns
+// a unit, CTA r taking the r-th of C ranges of K through a TMA ring into one
+// TMEM accumulator of 128 x n_pad. Afterwards the ring is free: each CTA puts
+// its partial into shared memory, token by token, and after a cluster barrier
+// CTA r sums the C partials of its 128/C rows through distributed shared
+// memory in rank order (one fixed order: deterministic, no atomics), applies
+// the epilogue in fp32 and writes the outputs.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 2..5 TMEM to shared memory, then all
+// eight reduce. Every wait is bounded; a cluster with a wait that gave up
+// writes NaN.
+#include <algorithm>
+
+#include "dense_core.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 64;
+constexpr int kThreads = 256;
+constexpr int kA = kTileM * kBK * 2;  // 16 KB of weights a stage
+constexpr int kLd = kTileM + 4;       // floats between two tokens' partial rows
+constexpr int kMaxStages = 12;
+
+struct SmallParams {
+  int T, N, num_kb;
+  int n_pad;         // T rounded up to a multiple of 16 (MMA N)
+  uint32_t n_alloc;  // TMEM columns (power of two >= 32)
+  int stages;
+  int act, stall;
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* out;
+  float* save;  // linear z [T, N]; gated [T, 2N]
+  unsigned long long timeout_ns;
+};
+
+// Two CTAs fit an SM up to 64 tokens, one above.
+__host__ __device__ constexpr int ring_bytes(int n_pad) { return n_pad <= 64 ? 98304 : 196608; }
+__host__ __device__ constexpr int ring_stages(int n_pad) {
+  return ring_bytes(n_pad) / (kA + n_pad * kBK * 2) < kMaxStages ? ring_bytes(n_pad) / (kA + n_pad * kBK * 2)
+                                                                  : kMaxStages;
+}
+size_t small_smem(int n_pad) { return 1024 + static_cast<size_t>(ring_bytes(n_pad)) + (2 * kMaxStages + 1) * 8 + 32; }
+
+__device__ __forceinline__ float4 sum_ranks(uint32_t addr, int csize) {
+  float4 v = ld_cluster_f32x4(cluster_map(addr, 0u));
+  for (int q = 1; q < csize; ++q) {
+    const float4 u = ld_cluster_f32x4(cluster_map(addr, static_cast<uint32_t>(q)));
+    v.x += u.x;
+    v.y += u.y;
+    v.z += u.z;
+    v.w += u.w;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float act_any(int act, float z) {
+  return act == kActNone ? z : gated_act(act, z, 1.0f);
+}
+
+template <bool kAmn, bool kGated>
+__global__ void __launch_bounds__(kThreads)
+    dense_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                       const SmallParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int kB = p.n_pad * kBK * 2;
+  const int kStages = p.stages;
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kStages * kA;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(p.n_pad));
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_status = reinterpret_cast<int*>(s_tmem + 2);
+  float* s_part = reinterpret_cast<float*>(smem);  // [T][kLd], after the last MMA
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int csize = static_cast<int>(cluster_nctarank());
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int unit = blockIdx.x / csize;
+  constexpr int kUnitRows = kGated ? 64 : 128;  // outputs of a unit
+  const int n0 = unit * kUnitRows;
+  const int kb0 = rank * p.num_kb / csize, kb1 = (rank + 1) * p.num_kb / csize;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    *s_abort = 0;
+    *s_status = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, p.n_alloc);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0 && !p.stall) {
+      int stage = 0;
+      uint32_t ph = 0;
+      int kb = kb0;
+      for (; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) break;
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(kA + kB));
+        uint8_t* a = sA + stage * kA;
+        const int k0 = kb * kBK;
+        if (kAmn) {
+          tma_load_2d(a, &tmW, &full[stage], n0, k0);
+          tma_load_2d(a + 8192, &tmW, &full[stage], n0 + 64, k0);
+        } else if (kGated) {
+          tma_load_2d(a, &tmW, &full[stage], k0, n0);
+          tma_load_2d(a + 8192, &tmW, &full[stage], k0, p.N + n0);
+        } else {
+          tma_load_2d(a, &tmW, &full[stage], k0, n0);
+        }
+        tma_load_2d(sB + stage * kB, &tmX, &full[stage], k0, 0);
+        if (++stage == kStages) {
+          stage = 0;
+          ph ^= 1;
+        }
+      }
+      if (kb < kb1) {
+        // let the copies already issued land before the shared memory is reused
+        for (int i = 0; i < kStages; ++i) {
+          if (--stage < 0) {
+            stage = kStages - 1;
+            ph ^= 1;
+          }
+          int never = 0;
+          mbar_wait_bounded(&full[stage], ph, &never, s_status, 1000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32_major(kTileM, p.n_pad, kAmn, false);
+      int stage = 0;
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&full[stage], ph, s_abort, s_status, p.timeout_ns)) break;
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(sA + stage * kA);
+        const uint32_t b0 = smem_u32(sB + stage * kB);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          umma_bf16(tmem_base, kAmn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32),
+                    sdesc_kmajor_sw128(b0 + k * 32), idesc, (kb > kb0 || k != 0) ? 1u : 0u);
+        umma_commit(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          ph ^= 1;
+        }
+      }
+      umma_commit(tfull);
+    }
+  } else if (warp < 6) {
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const bool got = mbar_wait_bounded(tfull, 0, s_abort, s_status, p.timeout_ns) && *s_abort == 0;
+    if (__all_sync(0xffffffffu, got)) {
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+      for (int c = 0; c < p.n_pad; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tb + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < p.T) s_part[(c + i) * kLd + r] = __uint_as_float(v[i]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // every CTA of the cluster has its partial in shared memory
+
+  bool aborted = false;
+  for (int q = 0; q < csize; ++q)
+    aborted |= ld_cluster_s32(cluster_map(smem_u32(const_cast<int*>(s_abort)), static_cast<uint32_t>(q))) != 0;
+  // four consecutive outputs of one token per step
+  const int per = kUnitRows / csize / 4;
+  for (int i = threadIdx.x; i < p.T * per; i += kThreads) {
+    const int t = i / per, r = (rank * per + (i - t * per)) * 4;
+    const int n = n0 + r;
+    if (n >= p.N) continue;  // N is a multiple of 8
+    float v[4];
+    const size_t at = static_cast<size_t>(t) * p.N + n;
+    const uint32_t sp = smem_u32(s_part + t * kLd + r);
+    if (aborted) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = __int_as_float(0x7FC00000);
+    } else if (kGated) {
+      const float4 g = sum_ranks(sp, csize), u = sum_ranks(sp + 64 * 4, csize);
+      if (p.save != nullptr) {
+        float* s = p.save + 2 * static_cast<size_t>(t) * p.N + n;
+        *reinterpret_cast<float4*>(s) = g;
+        *reinterpret_cast<float4*>(s + p.N) = u;
+      }
+      v[0] = gated_act(p.act, g.x, u.x);
+      v[1] = gated_act(p.act, g.y, u.y);
+      v[2] = gated_act(p.act, g.z, u.z);
+      v[3] = gated_act(p.act, g.w, u.w);
+    } else {
+      float4 z = sum_ranks(sp, csize);
+      if (p.bias != nullptr) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+        z.x += bf16_lo(b.x);
+        z.y += bf16_hi(b.x);
+        z.z += bf16_lo(b.y);
+        z.w += bf16_hi(b.y);
+      }
+      if (p.save != nullptr) *reinterpret_cast<float4*>(p.save + at) = z;
+      v[0] = act_any(p.act, z.x);
+      v[1] = act_any(p.act, z.y);
+      v[2] = act_any(p.act, z.z);
+      v[3] = act_any(p.act, z.w);
+      if (p.residual != nullptr) {
+        const uint2 b = *reinterpret_cast<const uint2*>(p.residual + at);
+        v[0] += bf16_lo(b.x);
+        v[1] += bf16_hi(b.x);
+        v[2] += bf16_lo(b.y);
+        v[3] += bf16_hi(b.y);
+      }
+    }
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+  // no CTA leaves while another may still read its shared memory
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.n_alloc);
+  }
+}
+
+template <bool kAmn, bool kGated>
+cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
+  // here the weights are g.b (rows = outputs) and the tokens g.a
+  constexpr int kUnitRows = kGated ? 64 : 128;
+  SmallParams p{};
+  p.T = g.M;
+  p.N = g.N;
+  p.num_kb = (g.K + kBK - 1) / kBK;
+  p.n_pad = (g.M + 15) / 16 * 16;
+  p.n_alloc = 32;
+  while (p.n_alloc < static_cast<uint32_t>(p.n_pad)) p.n_alloc <<= 1;
+  p.stages = ring_stages(p.n_pad);
+  p.act = g.act;
+  p.stall = stall_gate_up_loads();
+  p.bias = static_cast<const __nv_bfloat16*>(g.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(g.residual);
+  p.out = static_cast<__nv_bfloat16*>(g.out);
+  p.save = g.save0;
+  p.timeout_ns = wait_limit_ns();
+  // the partial rows reuse the ring
+  if (p.n_pad > 256 || p.n_pad * kLd * 4 > ring_bytes(p.n_pad)) return cudaErrorInvalidValue;
+
+  const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  CUtensorMap tmW, tmX;
+  const bool ok =
+      (kAmn ? encode_tensor_map_2d(&tmW, bf16, 2, g.b, g.N, g.K, 64, kBK)
+            : encode_tensor_map_2d(&tmW, bf16, 2, g.b, g.K, kGated ? 2 * static_cast<uint64_t>(g.N) : g.N, kBK,
+                                   kUnitRows)) &&
+      encode_tensor_map_2d(&tmX, bf16, 2, g.a, g.K, g.M, kBK, p.n_pad);
+  if (!ok) return cudaErrorInvalidValue;
+
+  auto kernel = dense_small_kernel<kAmn, kGated>;
+  static unsigned long long done = 0;
+  cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
+  if (err != cudaSuccess) return err;
+  const int units = (g.N + kUnitRows - 1) / kUnitRows;
+  const int slots = num_sms * (p.n_pad <= 64 ? 2 : 1);
+  int csize = 8;
+  while (csize > 1 && (units * csize > slots || csize * 2 > p.num_kb)) csize >>= 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * csize));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = small_smem(p.n_pad);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(csize);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, p);
+}
+
+}  // namespace
+
+bool dense_small_supported(const DenseGemm& g) {
+  return g.order != kLinearTN && g.M <= kDenseSmallT;
+}
+
+cudaError_t launch_dense_small(const DenseGemm& g, int num_sms, cudaStream_t st) {
+  if (g.order == kGatedNT) return launch_t<false, true>(g, num_sms, st);
+  if (g.order == kLinearNT) return launch_t<false, false>(g, num_sms, st);
+  return launch_t<true, false>(g, num_sms, st);
+}
+
+}  // namespace moe

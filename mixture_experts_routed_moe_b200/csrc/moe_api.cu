@@ -50,10 +50,16 @@ std::atomic<int> g_sm_count[kMaxDevices];
 bool encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem_bytes, const void* base,
                           uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                           CUtensorMapSwizzle swizzle) {
+  return encode_tensor_map_2d_ld(map, dtype, elem_bytes, base, inner, outer, inner, box_inner, box_outer, swizzle);
+}
+
+bool encode_tensor_map_2d_ld(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem_bytes, const void* base,
+                             uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner, uint32_t box_outer,
+                             CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {inner * elem_bytes};
+  const cuuint64_t strides[1] = {ld * elem_bytes};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -103,12 +103,65 @@ cudaError_t launch_fused_decode(const moe_shape* s, const Plan& p, const void* x
                                 const float* topk_w, const void* w_gate_up, const void* w_down, void* out,
                                 uint8_t* ws, int num_sms, cudaStream_t st);
 
+// ---- dense operators around the routed experts ----
+
+constexpr int kActNone = MOE_ACT_NONE;
+constexpr int kNormBackwardBlocks = 296;  // row classes of the norm's weight gradient (two per SM of a B200)
+constexpr int kDenseSmallT = 64;          // tokens up to which the weight-streaming kernel runs
+
+// Operand orders of a dense GEMM with out [M, N].
+enum DenseOrder {
+  kGatedNT,   // a [M, K], b [2N, K]: act(a b_gate^T) * (a b_up^T)
+  kLinearNT,  // a [M, K], b [N, K]: a b^T with bias, activation and residual
+  kLinearNN,  // a [M, K], b [K, N]: a b
+  kLinearTN   // a [K, M], b [K, N]: a^T b
+};
+
+struct DenseGemm {
+  int order;
+  int M, N, K;
+  const void* a;
+  const void* b;
+  void* out;
+  int act = kActNone;
+  const void* bias = nullptr;      // [N] bf16
+  const void* residual = nullptr;  // [M, N] bf16, may be out
+  float* save0 = nullptr;          // fp32 pre-activations: linear [M, N], gated [M, 2N]
+  int force = -1;                  // tile shape (a measurement's choice), -1 the rule's
+};
+
+cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st);
+// The form for few tokens (M), weights streamed with K split over clusters.
+bool dense_small_supported(const DenseGemm& g);
+cudaError_t launch_dense_small(const DenseGemm& g, int num_sms, cudaStream_t st);
+
+cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T, int I, int act, int num_sms,
+                              cudaStream_t st);
+int linear_grad_rows(int T, int N);
+cudaError_t launch_linear_grad(const float* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
+                               int act, cudaStream_t st);
+
+// out[c] = bf16(sum over rows of partial[r, c]), fixed order.
+cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* out, cudaStream_t st);
+
+cudaError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int T, int H, float eps, void* y,
+                            void* residual_out, uint8_t* codes, float* scales, float* rstd, cudaStream_t st);
+int rms_norm_backward_blocks(int T);
+cudaError_t launch_rms_norm_backward(const void* dy, const void* s, const void* weight, const float* rstd,
+                                     const void* dresidual, int T, int H, void* dx, void* dw, float* partial,
+                                     cudaStream_t st);
+
 // Tensor-map encoding through the driver entry point (no link-time libcuda dependency).
 // 128-byte swizzle by default (every operand tile and bf16 output tile); the
 // 64-byte swizzle for tiles of 64-byte rows.
 bool encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem_bytes, const void* base,
                           uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
                           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
+// The same for a matrix whose rows lie `ld` elements apart.
+bool encode_tensor_map_2d_ld(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem_bytes, const void* base,
+                             uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner, uint32_t box_outer,
+                             CUtensorMapSwizzle swizzle);
 
 int device_sm_count();
 
