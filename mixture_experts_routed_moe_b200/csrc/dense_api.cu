@@ -102,13 +102,15 @@ moe_status moe_rms_norm(const void* x, const void* residual, const void* weight,
   for (const Span& o : {sy, so})
     for (const Span& i : {sx, sr})
       if (!same_or_disjoint(o, i)) return MOE_ERR_INVALID_ARG;
-  return done(launch_rms_norm(x, residual, weight, T, H, eps, y, residual_out, codes, scales, rstd,
+  const int sms = device_sm_count();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  return done(launch_rms_norm(x, residual, weight, T, H, eps, y, residual_out, codes, scales, rstd, sms,
                               static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H) {
   if (T < 0 || !dim_ok(H) || H > kMaxNormH) return 0;
-  return round256(f32_bytes(std::max(1, rms_norm_backward_blocks(T)), H));
+  return round256(f32_bytes(std::max(1, rms_norm_backward_blocks(T, H)), H));
 }
 
 moe_status moe_rms_norm_backward(const void* dy, const void* s, const void* weight, const float* rstd,

@@ -6,14 +6,14 @@
 //   gated:   out[t, n] = bf16(act(sum_k W[n,k] X[t,k]) * sum_k W[N+n,k] X[t,k])
 //
 // with W read K-major, or MN-major (linear only: dx = dz W of the backward
-// pass, where W^T's rows are the outputs). A unit is 128 weight rows (gated: 64
-// gate rows and the 64 up rows that belong to them); a cluster of C CTAs owns
-// a unit, CTA r taking the r-th of C ranges of K through a TMA ring into one
-// TMEM accumulator of 128 x n_pad. Afterwards the ring is free: each CTA puts
-// its partial into shared memory, token by token, and after a cluster barrier
-// CTA r sums the C partials of its 128/C rows through distributed shared
-// memory in rank order (one fixed order: deterministic, no atomics), applies
-// the epilogue in fp32 and writes the outputs.
+// pass, where W^T's rows are the outputs). A unit is up to 128 weight rows
+// (gated: as many gate rows as up rows); a cluster of C CTAs owns a unit, CTA r
+// taking the r-th of C ranges of K through a TMA ring into one TMEM
+// accumulator of 128 x n_pad. Afterwards the ring is free: each CTA puts its
+// partial into shared memory, token by token, and after a cluster barrier
+// the CTAs share out the unit's outputs: the C partials are read through
+// distributed shared memory and added in rank order (one fixed order:
+// deterministic, no atomics), the epilogue is applied in fp32.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 TMEM to shared memory, then all
 // eight reduce. Every wait is bounded; a cluster with a wait that gave up
@@ -35,7 +35,8 @@ struct SmallParams {
   int T, N, num_kb;
   int n_pad;         // T rounded up to a multiple of 16 (MMA N)
   uint32_t n_alloc;  // TMEM columns (power of two >= 32)
-  int stages;
+  int stages, ring;  // TMA ring: stages of kA + n_pad * 128 bytes in `ring` bytes
+  int rows;          // outputs of a unit, a multiple of 8
   int act, stall;
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
@@ -44,28 +45,82 @@ struct SmallParams {
   unsigned long long timeout_ns;
 };
 
-// Two CTAs fit an SM up to 64 tokens, one above.
-__host__ __device__ constexpr int ring_bytes(int n_pad) { return n_pad <= 64 ? 98304 : 196608; }
-__host__ __device__ constexpr int ring_stages(int n_pad) {
-  return ring_bytes(n_pad) / (kA + n_pad * kBK * 2) < kMaxStages ? ring_bytes(n_pad) / (kA + n_pad * kBK * 2)
-                                                                  : kMaxStages;
-}
-size_t small_smem(int n_pad) { return 1024 + static_cast<size_t>(ring_bytes(n_pad)) + (2 * kMaxStages + 1) * 8 + 32; }
+// Bytes of the ring: half an SM's shared memory (two CTAs of it, or one and the
+// next kernel's, which starts early), more only where the partial needs it.
+int ring_bytes(int T) { return T * kLd * 4 <= 98304 ? 98304 : 147456; }
+size_t small_smem(int ring) { return 1024 + static_cast<size_t>(ring) + (2 * kMaxStages + 1) * 8 + 32; }
 
-__device__ __forceinline__ float4 sum_ranks(uint32_t addr, int csize) {
-  float4 v = ld_cluster_f32x4(cluster_map(addr, 0u));
-  for (int q = 1; q < csize; ++q) {
-    const float4 u = ld_cluster_f32x4(cluster_map(addr, static_cast<uint32_t>(q)));
-    v.x += u.x;
-    v.y += u.y;
-    v.z += u.z;
-    v.w += u.w;
+// The C partials at one place, added in rank order; all loads are in flight together.
+template <int kC>
+__device__ __forceinline__ float4 sum_ranks(uint32_t addr) {
+  float4 v[kC];
+#pragma unroll
+  for (int q = 0; q < kC; ++q) v[q] = ld_cluster_f32x4(cluster_map(addr, static_cast<uint32_t>(q)));
+#pragma unroll
+  for (int q = 1; q < kC; ++q) {
+    v[0].x += v[q].x;
+    v[0].y += v[q].y;
+    v[0].z += v[q].z;
+    v[0].w += v[q].w;
   }
-  return v;
+  return v[0];
 }
 
 __device__ __forceinline__ float act_any(int act, float z) {
   return act == kActNone ? z : gated_act(act, z, 1.0f);
+}
+
+// This CTA's share of the unit's outputs, four consecutive ones of a token per step.
+template <bool kGated, int kC>
+__device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int rank, bool aborted) {
+  const int per = p.rows / 4;
+  const int items = p.T * per;
+  for (int i = rank * items / kC + threadIdx.x; i < (rank + 1) * items / kC; i += kThreads) {
+    const int t = i / per, r = (i - t * per) * 4;
+    const int n = n0 + r;
+    if (n >= p.N) continue;  // N is a multiple of 8
+    float v[4];
+    const size_t at = static_cast<size_t>(t) * p.N + n;
+    const uint32_t sp = smem_u32(s_part + t * kLd + r);
+    if (aborted) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = __int_as_float(0x7FC00000);
+    } else if (kGated) {
+      const float4 g = sum_ranks<kC>(sp), u = sum_ranks<kC>(sp + p.rows * 4);
+      if (p.save != nullptr) {
+        float* s = p.save + 2 * static_cast<size_t>(t) * p.N + n;
+        *reinterpret_cast<float4*>(s) = g;
+        *reinterpret_cast<float4*>(s + p.N) = u;
+      }
+      v[0] = gated_act(p.act, g.x, u.x);
+      v[1] = gated_act(p.act, g.y, u.y);
+      v[2] = gated_act(p.act, g.z, u.z);
+      v[3] = gated_act(p.act, g.w, u.w);
+    } else {
+      uint2 res = make_uint2(0u, 0u);
+      if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + at);
+      float4 z = sum_ranks<kC>(sp);
+      if (p.bias != nullptr) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+        z.x += bf16_lo(b.x);
+        z.y += bf16_hi(b.x);
+        z.z += bf16_lo(b.y);
+        z.w += bf16_hi(b.y);
+      }
+      if (p.save != nullptr) *reinterpret_cast<float4*>(p.save + at) = z;
+      v[0] = act_any(p.act, z.x);
+      v[1] = act_any(p.act, z.y);
+      v[2] = act_any(p.act, z.z);
+      v[3] = act_any(p.act, z.w);
+      if (p.residual != nullptr) {
+        v[0] += bf16_lo(res.x);
+        v[1] += bf16_hi(res.x);
+        v[2] += bf16_lo(res.y);
+        v[3] += bf16_hi(res.y);
+      }
+    }
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
 }
 
 template <bool kAmn, bool kGated>
@@ -78,7 +133,7 @@ __global__ void __launch_bounds__(kThreads)
   const int kStages = p.stages;
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(p.n_pad));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.ring);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
@@ -90,9 +145,10 @@ __global__ void __launch_bounds__(kThreads)
   const int csize = static_cast<int>(cluster_nctarank());
   const int rank = static_cast<int>(cluster_ctarank());
   const int unit = blockIdx.x / csize;
-  constexpr int kUnitRows = kGated ? 64 : 128;  // outputs of a unit
-  const int n0 = unit * kUnitRows;
+  const int n0 = unit * p.rows;
   const int kb0 = rank * p.num_kb / csize, kb1 = (rank + 1) * p.num_kb / csize;
+  // bytes a stage receives (an MN-major unit always has 128 rows)
+  const uint32_t stage_bytes = static_cast<uint32_t>((kGated ? 2 : 1) * (kAmn ? 128 : p.rows) * 128 + kB);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -125,7 +181,7 @@ __global__ void __launch_bounds__(kThreads)
       int kb = kb0;
       for (; kb < kb1; ++kb) {
         if (!mbar_wait_bounded(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) break;
-        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(kA + kB));
+        mbar_arrive_expect_tx(&full[stage], stage_bytes);
         uint8_t* a = sA + stage * kA;
         const int k0 = kb * kBK;
         if (kAmn) {
@@ -133,7 +189,7 @@ __global__ void __launch_bounds__(kThreads)
           tma_load_2d(a + 8192, &tmW, &full[stage], n0 + 64, k0);
         } else if (kGated) {
           tma_load_2d(a, &tmW, &full[stage], k0, n0);
-          tma_load_2d(a + 8192, &tmW, &full[stage], k0, p.N + n0);
+          tma_load_2d(a + p.rows * 128, &tmW, &full[stage], k0, p.N + n0);
         } else {
           tma_load_2d(a, &tmW, &full[stage], k0, n0);
         }
@@ -201,52 +257,18 @@ __global__ void __launch_bounds__(kThreads)
   bool aborted = false;
   for (int q = 0; q < csize; ++q)
     aborted |= ld_cluster_s32(cluster_map(smem_u32(const_cast<int*>(s_abort)), static_cast<uint32_t>(q))) != 0;
-  // four consecutive outputs of one token per step
-  const int per = kUnitRows / csize / 4;
-  for (int i = threadIdx.x; i < p.T * per; i += kThreads) {
-    const int t = i / per, r = (rank * per + (i - t * per)) * 4;
-    const int n = n0 + r;
-    if (n >= p.N) continue;  // N is a multiple of 8
-    float v[4];
-    const size_t at = static_cast<size_t>(t) * p.N + n;
-    const uint32_t sp = smem_u32(s_part + t * kLd + r);
-    if (aborted) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = __int_as_float(0x7FC00000);
-    } else if (kGated) {
-      const float4 g = sum_ranks(sp, csize), u = sum_ranks(sp + 64 * 4, csize);
-      if (p.save != nullptr) {
-        float* s = p.save + 2 * static_cast<size_t>(t) * p.N + n;
-        *reinterpret_cast<float4*>(s) = g;
-        *reinterpret_cast<float4*>(s + p.N) = u;
-      }
-      v[0] = gated_act(p.act, g.x, u.x);
-      v[1] = gated_act(p.act, g.y, u.y);
-      v[2] = gated_act(p.act, g.z, u.z);
-      v[3] = gated_act(p.act, g.w, u.w);
-    } else {
-      float4 z = sum_ranks(sp, csize);
-      if (p.bias != nullptr) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
-        z.x += bf16_lo(b.x);
-        z.y += bf16_hi(b.x);
-        z.z += bf16_lo(b.y);
-        z.w += bf16_hi(b.y);
-      }
-      if (p.save != nullptr) *reinterpret_cast<float4*>(p.save + at) = z;
-      v[0] = act_any(p.act, z.x);
-      v[1] = act_any(p.act, z.y);
-      v[2] = act_any(p.act, z.z);
-      v[3] = act_any(p.act, z.w);
-      if (p.residual != nullptr) {
-        const uint2 b = *reinterpret_cast<const uint2*>(p.residual + at);
-        v[0] += bf16_lo(b.x);
-        v[1] += bf16_hi(b.x);
-        v[2] += bf16_lo(b.y);
-        v[3] += bf16_hi(b.y);
-      }
-    }
-    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  switch (csize) {
+    case 1:
+      finish<kGated, 1>(p, s_part, n0, rank, aborted);
+      break;
+    case 2:
+      finish<kGated, 2>(p, s_part, n0, rank, aborted);
+      break;
+    case 4:
+      finish<kGated, 4>(p, s_part, n0, rank, aborted);
+      break;
+    default:
+      finish<kGated, 8>(p, s_part, n0, rank, aborted);
   }
   // no CTA leaves while another may still read its shared memory
   cluster_sync();
@@ -259,7 +281,6 @@ __global__ void __launch_bounds__(kThreads)
 template <bool kAmn, bool kGated>
 cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   // here the weights are g.b (rows = outputs) and the tokens g.a
-  constexpr int kUnitRows = kGated ? 64 : 128;
   SmallParams p{};
   p.T = g.M;
   p.N = g.N;
@@ -267,7 +288,8 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.n_pad = (g.M + 15) / 16 * 16;
   p.n_alloc = 32;
   while (p.n_alloc < static_cast<uint32_t>(p.n_pad)) p.n_alloc <<= 1;
-  p.stages = ring_stages(p.n_pad);
+  p.ring = ring_bytes(g.M);
+  p.stages = std::min(kMaxStages, p.ring / (kA + p.n_pad * kBK * 2));
   p.act = g.act;
   p.stall = stall_gate_up_loads();
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
@@ -276,14 +298,29 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.save = g.save0;
   p.timeout_ns = wait_limit_ns();
   // the partial rows reuse the ring
-  if (p.n_pad > 256 || p.n_pad * kLd * 4 > ring_bytes(p.n_pad)) return cudaErrorInvalidValue;
+  if (p.n_pad > 256 || g.M * kLd * 4 > p.ring) return cudaErrorInvalidValue;
+
+  // The widest cluster whose CTAs all fit two to an SM and have K steps to
+  // share. Many tokens make the reduction of eight partials dearer than it
+  // saves; linear units are halved there while the CTAs do not fill the SMs.
+  const int cmax = g.M <= 32 ? 8 : 4;
+  p.rows = kGated ? 64 : 128;
+  auto units_of = [&](int rows) { return (g.N + rows - 1) / rows; };
+  int csize = cmax;
+  while (csize > 1 && (static_cast<long long>(units_of(p.rows)) * csize > 2ll * num_sms || csize * 2 > p.num_kb))
+    csize >>= 1;
+  if (!kGated && !kAmn && csize == 4 && units_of(128) * csize < num_sms * 4 / 5) p.rows = 64;
+  if (g.force >= 0) {  // csize in the low byte, rows above
+    csize = g.force & 255;
+    p.rows = g.force >> 8;
+  }
 
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap tmW, tmX;
   const bool ok =
       (kAmn ? encode_tensor_map_2d(&tmW, bf16, 2, g.b, g.N, g.K, 64, kBK)
             : encode_tensor_map_2d(&tmW, bf16, 2, g.b, g.K, kGated ? 2 * static_cast<uint64_t>(g.N) : g.N, kBK,
-                                   kUnitRows)) &&
+                                   p.rows)) &&
       encode_tensor_map_2d(&tmX, bf16, 2, g.a, g.K, g.M, kBK, p.n_pad);
   if (!ok) return cudaErrorInvalidValue;
 
@@ -291,14 +328,11 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   static unsigned long long done = 0;
   cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
   if (err != cudaSuccess) return err;
-  const int units = (g.N + kUnitRows - 1) / kUnitRows;
-  const int slots = num_sms * (p.n_pad <= 64 ? 2 : 1);
-  int csize = 8;
-  while (csize > 1 && (units * csize > slots || csize * 2 > p.num_kb)) csize >>= 1;
+  const int units = (g.N + p.rows - 1) / p.rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * csize));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = small_smem(p.n_pad);
+  cfg.dynamicSmemBytes = small_smem(p.ring);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

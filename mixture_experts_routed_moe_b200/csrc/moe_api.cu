@@ -88,7 +88,11 @@ cudaError_t ensure_max_smem(const void* kernel, unsigned long long* done) {
   int optin = 0;
   err = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (err != cudaSuccess) return err;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+  cudaFuncAttributes attr{};
+  err = cudaFuncGetAttributes(&attr, kernel);  // static shared memory comes out of the same limit
+  if (err != cudaSuccess) return err;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             optin - static_cast<int>(attr.sharedSizeBytes));
   if (err == cudaSuccess && bit != 0) __atomic_fetch_or(done, bit, __ATOMIC_ACQ_REL);
   return err;
 }

@@ -145,8 +145,9 @@ cudaError_t launch_linear_grad(const float* z, const void* dy, void* dz, float* 
 cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* out, cudaStream_t st);
 
 cudaError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int T, int H, float eps, void* y,
-                            void* residual_out, uint8_t* codes, float* scales, float* rstd, cudaStream_t st);
-int rms_norm_backward_blocks(int T);
+                            void* residual_out, uint8_t* codes, float* scales, float* rstd, int num_sms,
+                            cudaStream_t st);
+int rms_norm_backward_blocks(int T, int H);
 cudaError_t launch_rms_norm_backward(const void* dy, const void* s, const void* weight, const float* rstd,
                                      const void* dresidual, int T, int H, void* dx, void* dw, float* partial,
                                      cudaStream_t st);

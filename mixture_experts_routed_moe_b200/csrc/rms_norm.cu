@@ -50,88 +50,56 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Sum over the `nthr` threads (a multiple of 32) that share a row, the same
-// value in all of them; one warp needs no shared memory. The warp sums are
-// added in warp order. `s_red` holds one float per warp and is free again
-// after the row's next barrier.
-__device__ __forceinline__ float row_sum(float v, int nthr, float* s_red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (nthr == 32) return v;
-  const int warp = threadIdx.x >> 5, nw = nthr >> 5;
-  if ((threadIdx.x & 31) == 0) s_red[warp] = v;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  float t = lane < nw ? s_red[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t;
-}
-
-// One row per `tpr` threads: a warp with rows_per_block rows in a block, or the
-// whole block. Thread i of the row holds the 16-byte vectors i, i + tpr, ...;
-// the 16 vectors of a 128-column group lie in one half-warp.
+// Sum over the threads that share a row, the same value in all of them. One
+// warp: a butterfly over the lanes' sums of v. A block (tpr threads, a multiple
+// of 32; one barrier of the whole block): v[j] of a warp belongs to the 32
+// consecutive vectors of chunk j * tpr / 32 + warp; the chunks' sums are added in
+// an order of their own numbers, so that a row's sum does not depend on how
+// many vectors a thread holds. s_red holds a float for each chunk of the
+// block's rows; two such buffers in turn make one barrier a row enough.
 template <int kVec>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p, int tpr) {
-  pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
-  pdl_trigger();
-  __shared__ float s_red[32];
-  const int rpb = blockDim.x / tpr;
-  const long long t = static_cast<long long>(blockIdx.x) * rpb + threadIdx.x / tpr;
-  if (t >= p.T) return;  // whole warps leave; a block-wide row always exists
-  const int i0 = threadIdx.x % tpr;
-  const int nvec = p.H / 8;
-  const size_t base = static_cast<size_t>(t) * p.H;
-  const uint4* x = reinterpret_cast<const uint4*>(p.x + base);
-  const uint4* res = reinterpret_cast<const uint4*>(p.residual + base);
-  const uint4* wv = reinterpret_cast<const uint4*>(p.weight);
+struct RowSum {
+  int nw, warp, lane, first;  // warps of a row, this one's number in it, the row's first slot
 
-  uint4 s[kVec], w[kVec];
-  uint4 rv[kVec];
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const int i = i0 + j * tpr;
-    s[j] = i < nvec ? x[i] : make_uint4(0u, 0u, 0u, 0u);
+  __device__ __forceinline__ explicit RowSum(int tpr)
+      : nw(tpr >> 5), lane(threadIdx.x & 31) {
+    const int group = (threadIdx.x >> 5) / nw;
+    warp = (threadIdx.x >> 5) - group * nw;
+    first = group * nw * kVec;
   }
-  if (p.residual != nullptr) {
+  static __device__ __forceinline__ float butterfly(float t) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int i = i0 + j * tpr;
-      rv[j] = i < nvec ? res[i] : make_uint4(0u, 0u, 0u, 0u);
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+  }
+  __device__ __forceinline__ float operator()(const float (&v)[kVec], float* s_red) const {
+    if (nw == 1) {
+      float t = v[0];
+#pragma unroll
+      for (int j = 1; j < kVec; ++j) t += v[j];
+      return butterfly(t);
     }
-  }
+    float* red = s_red + first;
+    float c[kVec];
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const int i = i0 + j * tpr;
-    w[j] = i < nvec ? __ldg(wv + i) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float sum = 0.f;
+    for (int j = 0; j < kVec; ++j) c[j] = butterfly(v[j]);
+    if (lane == 0) {
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    float a[8];
-    unpack8(s[j], a);
-    if (p.residual != nullptr) {
-      float b[8];
-      unpack8(rv[j], b);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) a[q] += b[q];
-      s[j] = pack8(a);
-      unpack8(s[j], a);
+      for (int j = 0; j < kVec; ++j) red[j * nw + warp] = c[j];
     }
+    __syncthreads();
+    float t = lane < nw * kVec ? red[lane] : 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum = fmaf(a[q], a[q], sum);
+    for (int q = 1; q < kVec; ++q)
+      if (lane + 32 * q < nw * kVec) t += red[lane + 32 * q];
+    return butterfly(t);
   }
-  if (p.residual_out != nullptr) {
-    uint4* ro = reinterpret_cast<uint4*>(p.residual_out + base);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int i = i0 + j * tpr;
-      if (i < nvec) ro[i] = s[j];
-    }
-  }
-  sum = row_sum(sum, tpr, s_red);
-  const float r = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
-  if (p.rstd != nullptr && i0 == 0) p.rstd[t] = r;
+};
+
+// Scales one thread's vectors of row t and writes y, the codes and the scales.
+template <int kVec, bool kCodes>
+__device__ __forceinline__ void norm_write(const NormParams& p, const uint4 (&s)[kVec], const uint4 (&w)[kVec], float r,
+                                           size_t base, int i0, int tpr, int nvec) {
   const unsigned hmask = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
@@ -142,8 +110,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p, int 
     unpack8(w[j], g);
 #pragma unroll
     for (int q = 0; q < 8; ++q) a[q] = a[q] * r * g[q];
-    if (p.y != nullptr) reinterpret_cast<uint4*>(p.y + base)[i] = pack8(a);
-    if (p.codes != nullptr) {
+    if (!kCodes || p.y != nullptr) reinterpret_cast<uint4*>(p.y + base)[i] = pack8(a);
+    if (kCodes) {
       float amax = 0.f;
 #pragma unroll
       for (int q = 0; q < 8; ++q) amax = fmaxf(amax, fabsf(a[q]));
@@ -166,6 +134,81 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p, int 
   }
 }
 
+// s = x + residual rounded to bf16 (x where the row has none), and the sum of its squares.
+template <bool kRes>
+__device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, float& sum) {
+  float a[8];
+  unpack8(x, a);
+  uint4 s = x;
+  if (kRes) {
+    float b[8];
+    unpack8(res, b);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) a[q] += b[q];
+    s = pack8(a);
+    unpack8(s, a);
+  }
+  sum = a[0] * a[0];
+#pragma unroll
+  for (int q = 1; q < 8; ++q) sum = fmaf(a[q], a[q], sum);
+  return s;
+}
+
+// A row is held by `tpr` threads: one warp, with blockDim / 32 rows in a
+// block, or the whole block. Thread i of the row holds the 16-byte vectors i,
+// i + tpr, ...; the 16 vectors of a 128-column group lie in one half-warp. The
+// grid is a few blocks an SM; each row group walks over its rows with the next
+// row's loads in flight while it reduces and stores the current one.
+template <int kVec, int kMaxThreads, bool kRes, bool kCodes>
+__global__ void __launch_bounds__(kMaxThreads, !kRes && kVec == 1 && kMaxThreads == 512 ? 3 : 1) rms_norm_kernel(const NormParams p, int tpr) {
+  pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
+  pdl_trigger();
+  __shared__ float s_red[2][32 * kVec];
+  const int rpb = blockDim.x / tpr;
+  const RowSum<kVec> row_sum(tpr);
+  const int i0 = threadIdx.x % tpr;
+  const int nvec = p.H / 8;
+  const long long step = static_cast<long long>(gridDim.x) * rpb;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 w[kVec], xv[kVec], rv[kVec];
+  auto load = [&](long long t) {
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * p.H);
+    const uint4* r = reinterpret_cast<const uint4*>(p.residual + static_cast<size_t>(t) * p.H);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int i = i0 + j * tpr;
+      xv[j] = i < nvec ? x[i] : zero;
+      if (kRes) rv[j] = i < nvec ? r[i] : zero;
+    }
+  };
+  long long t = static_cast<long long>(blockIdx.x) * rpb + threadIdx.x / tpr;
+  if (t < p.T) load(t);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    const int i = i0 + j * tpr;
+    w[j] = i < nvec ? __ldg(reinterpret_cast<const uint4*>(p.weight) + i) : zero;
+  }
+  const float inv_h = 1.0f / static_cast<float>(p.H);
+  int flip = 0;
+  // a row group of a block-wide row leaves the loop together, a warp on its own
+  for (; t < p.T; t += step, flip ^= 1) {
+    const size_t base = static_cast<size_t>(t) * p.H;
+    uint4 s[kVec];
+    float sq[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      s[j] = add_residual<kRes>(xv[j], rv[j], sq[j]);
+      const int i = i0 + j * tpr;
+      if (kRes && p.residual_out != nullptr && i < nvec) reinterpret_cast<uint4*>(p.residual_out + base)[i] = s[j];
+    }
+    if (t + step < p.T) load(t + step);
+    const float sum = row_sum(sq, s_red[flip]);
+    const float r = rsqrtf(fmaf(sum, inv_h, p.eps));
+    if (p.rstd != nullptr && i0 == 0) p.rstd[t] = r;
+    norm_write<kVec, kCodes>(p, s, w, r, base, i0, tpr, nvec);
+  }
+}
+
 struct NormBwdParams {
   const __nv_bfloat16* dy;
   const __nv_bfloat16* s;
@@ -177,117 +220,181 @@ struct NormBwdParams {
   int T, H;
 };
 
-// Block b takes the rows b, b + grid, ...: dx of each row, and the block's sum
-// of dy s r over its rows in registers, written once as a partial row that
-// column_sum_kernel adds over the blocks.
-template <int kVec>
-__global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBwdParams p) {
+// A row is held by `tpr` threads, with blockDim / tpr rows in a block at a time;
+// a row group takes every (grid x groups)-th row: dx of each, and the sum of dy s
+// r over its rows in registers. The block adds its groups' sums in order and
+// writes one partial row, which column_sum_kernel adds over the blocks. With
+// kPrefetch the next row's loads are in flight during the reduction and the
+// stores of the current one; without (rows so wide that the sums of dw take the
+// registers) the second pass over the row reads it again, from the caches.
+template <int kVec, int kMaxThreads, bool kPrefetch>
+__global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const NormBwdParams p, int tpr) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_red[2][32];
-  const int nvec = p.H / 8, tpr = blockDim.x;
+  extern __shared__ float s_dw[];  // [groups - 1][H]
+  __shared__ float s_red[2][32 * kVec];
+  const int nvec = p.H / 8, groups = blockDim.x / tpr;
+  const int group = threadIdx.x / tpr, i0 = threadIdx.x - group * tpr;
+  const RowSum<kVec> row_sum(tpr);
+  const long long step = static_cast<long long>(gridDim.x) * groups;
   const uint4* wv = reinterpret_cast<const uint4*>(p.weight);
-  uint4 w[kVec];
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  constexpr int kHeld = kPrefetch ? kVec : 1;
+  uint4 ndy[kHeld], ns[kHeld], ndr[kHeld], w[kHeld];
+  float nr = 0.f;
+  auto vec_of = [&](const __nv_bfloat16* m, long long t, int i) {
+    return t < p.T && i < nvec && m != nullptr
+               ? reinterpret_cast<const uint4*>(m + static_cast<size_t>(t) * p.H)[i]
+               : zero;
+  };
+  auto load = [&](long long t) {
+    nr = t < p.T ? __ldg(p.rstd + t) : 0.f;
+#pragma unroll
+    for (int j = 0; j < (kPrefetch ? kVec : 0); ++j) {
+      ndy[j] = vec_of(p.dy, t, i0 + j * tpr);
+      ns[j] = vec_of(p.s, t, i0 + j * tpr);
+      ndr[j] = vec_of(p.dresidual, t, i0 + j * tpr);
+    }
+  };
+  long long t0 = static_cast<long long>(blockIdx.x) * groups;  // the block's first row of this step
+  load(t0 + group);
   float dw[kVec][8];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int i = threadIdx.x + j * tpr;
-    w[j] = i < nvec ? __ldg(wv + i) : make_uint4(0u, 0u, 0u, 0u);
+    if (kPrefetch) w[j] = i0 + j * tpr < nvec ? __ldg(wv + i0 + j * tpr) : zero;
 #pragma unroll
     for (int q = 0; q < 8; ++q) dw[j][q] = 0.f;
   }
   const float inv_h = 1.0f / static_cast<float>(p.H);
   int flip = 0;
-  for (long long t = blockIdx.x; t < p.T; t += gridDim.x, flip ^= 1) {
-    const size_t base = static_cast<size_t>(t) * p.H;
-    const uint4* dyp = reinterpret_cast<const uint4*>(p.dy + base);
-    const uint4* sp = reinterpret_cast<const uint4*>(p.s + base);
-    const uint4* rp = reinterpret_cast<const uint4*>(p.dresidual + base);
-    uint4 dy[kVec], s[kVec], dr[kVec];
+  while (t0 < p.T) {
+    const long long t = t0 + group;
+    uint4 dy[kHeld], s[kHeld], dr[kHeld];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const int i = threadIdx.x + j * tpr;
-      const bool in = i < nvec;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      dy[j] = in ? dyp[i] : zero;
-      s[j] = in ? sp[i] : zero;
-      dr[j] = in && p.dresidual != nullptr ? rp[i] : zero;
+    for (int j = 0; j < (kPrefetch ? kVec : 0); ++j) {
+      dy[j] = ndy[j];
+      s[j] = ns[j];
+      dr[j] = ndr[j];
     }
-    const float r = p.rstd[t];
-    float dot = 0.f;
+    const float r = nr;
+    t0 += step;
+    if (t0 < p.T) load(t0 + group);
+    float part[kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
+      const int i = i0 + j * tpr;
       float a[8], b[8], g[8];
-      unpack8(dy[j], a);
-      unpack8(s[j], b);
-      unpack8(w[j], g);
+      part[j] = 0.f;
+      unpack8(kPrefetch ? dy[kPrefetch ? j : 0] : vec_of(p.dy, t, i), a);
+      unpack8(kPrefetch ? s[kPrefetch ? j : 0] : vec_of(p.s, t, i), b);
+      unpack8(kPrefetch ? w[kPrefetch ? j : 0] : vec_of(p.weight, 0, i), g);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float xh = b[q] * r;
         dw[j][q] = fmaf(a[q], xh, dw[j][q]);
-        dot = fmaf(a[q] * g[q], xh, dot);
+        part[j] = fmaf(a[q] * g[q], xh, part[j]);
       }
     }
-    // two buffers in turn: a warp may still read one row's sums while another
-    // writes the next row's
-    dot = row_sum(dot, tpr, s_red[flip]) * inv_h;
+    const float dot = row_sum(part, s_red[flip]) * inv_h;
+    flip ^= 1;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      const int i = threadIdx.x + j * tpr;
-      if (i >= nvec) continue;
+      const int i = i0 + j * tpr;
+      if (t >= p.T || i >= nvec) continue;
       float a[8], b[8], g[8], d[8];
-      unpack8(dy[j], a);
-      unpack8(s[j], b);
-      unpack8(w[j], g);
-      unpack8(dr[j], d);
+      unpack8(kPrefetch ? dy[kPrefetch ? j : 0] : vec_of(p.dy, t, i), a);
+      unpack8(kPrefetch ? s[kPrefetch ? j : 0] : vec_of(p.s, t, i), b);
+      unpack8(kPrefetch ? w[kPrefetch ? j : 0] : vec_of(p.weight, 0, i), g);
+      unpack8(kPrefetch ? dr[kPrefetch ? j : 0] : vec_of(p.dresidual, t, i), d);
 #pragma unroll
       for (int q = 0; q < 8; ++q) d[q] = fmaf(r, a[q] * g[q] - b[q] * r * dot, d[q]);
-      reinterpret_cast<uint4*>(p.dx + base)[i] = pack8(d);
+      reinterpret_cast<uint4*>(p.dx + static_cast<size_t>(t) * p.H)[i] = pack8(d);
     }
+  }
+  if (groups > 1) {
+    if (group > 0) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const int i = i0 + j * tpr;
+        if (i >= nvec) continue;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s_dw[(group - 1) * p.H + 8 * i + q] = dw[j][q];
+      }
+    }
+    __syncthreads();
+    if (group > 0) return;
   }
   float* out = p.partial + static_cast<size_t>(blockIdx.x) * p.H;
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    const int i = threadIdx.x + j * tpr;
+    const int i = i0 + j * tpr;
     if (i >= nvec) continue;
+    for (int g = 0; g < groups - 1; ++g)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) dw[j][q] += s_dw[g * p.H + 8 * i + q];
     reinterpret_cast<float4*>(out)[2 * i] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
     reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
   }
 }
 
-// out[c] = bf16(sum_r partial[r][c]), r ascending within each of eight row
+// out[c] = bf16(sum_r partial[r][c]), r ascending within each of 32 row
 // classes, the classes added in order. A block takes 32 columns.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ partial, int rows, int cols,
-                                                         __nv_bfloat16* __restrict__ out) {
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int rows, int cols,
+                                                          __nv_bfloat16* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_sum[8][33];
+  __shared__ float s_sum[32][33];
   const int lane = threadIdx.x & 31, cls = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < cols)
-    for (int r = cls; r < rows; r += 8) v += partial[static_cast<size_t>(r) * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int r = cls; r < rows; r += 32) v += partial[static_cast<size_t>(r) * cols + c];
+  }
   s_sum[cls][lane] = v;
   __syncthreads();
   if (cls == 0 && c < cols) {
-    float t = s_sum[0][lane];
+    float t = 0.f;
 #pragma unroll
-    for (int q = 1; q < 8; ++q) t += s_sum[q][lane];
+    for (int q = 0; q < 32; ++q) t += s_sum[q][lane];
     out[c] = __float2bfloat16_rn(t);
   }
 }
+
+// Threads of the norm's grid per SM. Without a residual a row has half the bytes,
+// so more rows have to be in flight (8192 x 2048: 13.4 us with 1536 threads, 17.1 with 1024).
+constexpr int norm_threads(bool res) { return res ? 1024 : 1536; }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
 
 }  // namespace
 
 cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* out, cudaStream_t st) {
-  return launch_pdl(column_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(256), 0, st, partial, rows,
+  return launch_pdl(column_sum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(1024), 0, st, partial, rows,
                     cols, static_cast<__nv_bfloat16*>(out));
 }
 
+namespace {
+
+template <int kVec, int kMaxThreads>
+cudaError_t launch_norm_t(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
+  const long long rpb = block / tpr;
+  const int per_sm = std::max(1, norm_threads(p.residual != nullptr) / block);
+  const long long blocks = std::min<long long>((p.T + rpb - 1) / rpb, static_cast<long long>(num_sms) * per_sm);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(static_cast<unsigned>(block)), 0, st, p, tpr); };
+  if (p.residual != nullptr)
+    return p.codes != nullptr ? go(rms_norm_kernel<kVec, kMaxThreads, true, true>)
+                              : go(rms_norm_kernel<kVec, kMaxThreads, true, false>);
+  return p.codes != nullptr ? go(rms_norm_kernel<kVec, kMaxThreads, false, true>)
+                            : go(rms_norm_kernel<kVec, kMaxThreads, false, false>);
+}
+
+}  // namespace
+
 cudaError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int T, int H, float eps, void* y,
-                            void* residual_out, uint8_t* codes, float* scales, float* rstd, cudaStream_t st) {
+                            void* residual_out, uint8_t* codes, float* scales, float* rstd, int num_sms,
+                            cudaStream_t st) {
   NormParams p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.residual = static_cast<const __nv_bfloat16*>(residual);
@@ -301,31 +408,37 @@ cudaError_t launch_rms_norm(const void* x, const void* residual, const void* wei
   p.H = H;
   p.eps = eps;
   const int nvec = H / 8;
-  // a warp per row up to four vectors a lane, else a block per row with at
-  // least eight warps' worth of vectors spread over it
-  int vec, tpr, block;
-  if (nvec <= 128) {
-    vec = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
-    tpr = 32;
-    block = 128;
-  } else {
-    vec = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 4096 ? 4 : 8;
-    tpr = block = round32((nvec + vec - 1) / vec);
-  }
-  const dim3 grid(static_cast<unsigned>((static_cast<long long>(T) + block / tpr - 1) / (block / tpr)));
-  switch (vec) {
-    case 1:
-      return launch_pdl(rms_norm_kernel<1>, grid, dim3(block), 0, st, p, tpr);
-    case 2:
-      return launch_pdl(rms_norm_kernel<2>, grid, dim3(block), 0, st, p, tpr);
-    case 4:
-      return launch_pdl(rms_norm_kernel<4>, grid, dim3(block), 0, st, p, tpr);
-    default:
-      return launch_pdl(rms_norm_kernel<8>, grid, dim3(block), 0, st, p, tpr);
-  }
+  // a warp per row up to four vectors a lane, else a block per row
+  if (nvec <= 32) return launch_norm_t<1, 512>(p, 128, 32, num_sms, st);
+  if (nvec <= 64) return launch_norm_t<2, 512>(p, 128, 32, num_sms, st);
+  if (nvec <= 128) return launch_norm_t<4, 512>(p, 128, 32, num_sms, st);
+  auto threads = [&](int vec) { return round32((nvec + vec - 1) / vec); };
+  if (nvec <= 512) return launch_norm_t<1, 512>(p, threads(1), threads(1), num_sms, st);
+  // One vector a thread shortens a row's path, which counts where few rows run
+  // (16 x 7168 with codes: 2.8 us against 3.7 with four) and where the codes'
+  // arithmetic paces it (4096 x 7168: 47.0 against 48.1); four keep more bytes
+  // in flight (4096 x 7168 without codes: 37.6 us against 43).
+  if (nvec <= 1024 && (codes != nullptr || T <= 2 * num_sms))
+    return launch_norm_t<1, 1024>(p, threads(1), threads(1), num_sms, st);
+  if (nvec <= 2048) return launch_norm_t<4, 512>(p, threads(4), threads(4), num_sms, st);
+  return launch_norm_t<8, 1024>(p, threads(8), threads(8), num_sms, st);
 }
 
-int rms_norm_backward_blocks(int T) { return std::min(T, kNormBackwardBlocks); }
+namespace {
+
+// Threads that share a row of the backward pass, and rows of a block at a time:
+// blocks of 256 threads and more.
+int backward_vec(int nvec) { return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8; }
+int backward_tpr(int nvec) { return round32((nvec + backward_vec(nvec) - 1) / backward_vec(nvec)); }
+int backward_groups(int nvec) { return std::max(1, 256 / backward_tpr(nvec)); }
+
+}  // namespace
+
+// Partial rows of the weight gradient: the blocks, at most 1024 threads an SM.
+int rms_norm_backward_blocks(int T, int H) {
+  const int nvec = H / 8, groups = backward_groups(nvec), block = groups * backward_tpr(nvec);
+  return std::min((T + groups - 1) / groups, kNormBackwardBlocks / 2 * std::max(1, std::min(4, 1024 / block)));
+}
 
 cudaError_t launch_rms_norm_backward(const void* dy, const void* s, const void* weight, const float* rstd,
                                      const void* dresidual, int T, int H, void* dx, void* dw, float* partial,
@@ -340,23 +453,25 @@ cudaError_t launch_rms_norm_backward(const void* dy, const void* s, const void* 
   p.partial = partial;
   p.T = T;
   p.H = H;
-  const int nvec = H / 8;
-  const int vec = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : nvec <= 4096 ? 4 : 8;
-  const dim3 grid(static_cast<unsigned>(rms_norm_backward_blocks(T)));
-  const dim3 block(static_cast<unsigned>(round32((nvec + vec - 1) / vec)));
+  const int nvec = H / 8, tpr = backward_tpr(nvec), groups = backward_groups(nvec);
+  const dim3 grid(static_cast<unsigned>(rms_norm_backward_blocks(T, H)));
+  const size_t smem = static_cast<size_t>(groups - 1) * H * sizeof(float);  // below 8 KB: H <= 1024 where groups > 1
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, grid, dim3(static_cast<unsigned>(tpr * groups)), smem, st, p, tpr);
+  };
   cudaError_t err;
-  switch (vec) {
+  switch (backward_vec(nvec)) {
     case 1:
-      err = launch_pdl(rms_norm_backward_kernel<1>, grid, block, 0, st, p);
+      err = go(rms_norm_backward_kernel<1, 512, true>);
       break;
     case 2:
-      err = launch_pdl(rms_norm_backward_kernel<2>, grid, block, 0, st, p);
+      err = go(rms_norm_backward_kernel<2, 512, true>);
       break;
     case 4:
-      err = launch_pdl(rms_norm_backward_kernel<4>, grid, block, 0, st, p);
+      err = go(rms_norm_backward_kernel<4, 512, false>);
       break;
     default:
-      err = launch_pdl(rms_norm_backward_kernel<8>, grid, block, 0, st, p);
+      err = go(rms_norm_backward_kernel<8, 1024, false>);
   }
   if (err != cudaSuccess) return err;
   return launch_column_sum(partial, static_cast<int>(grid.x), H, dw, st);

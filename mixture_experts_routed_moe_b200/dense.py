@@ -60,11 +60,12 @@ def _launch(device, stream):
     return guard, torch._C._cuda_getCurrentRawStream(index)
 
 
-def _output(t, name, dtype, shape, device):
-    """The caller's output tensor after its checks, or a new one."""
+def _output(t, name, like, shape, device):
+    """The caller's bf16 output tensor after its checks, or a new one (of
+    like's type and device: `like` is an input)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(t, name, dtype, shape, device)
+        return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+    _tensor(t, name, _BF16, shape, device)
     return t
 
 
@@ -107,10 +108,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
     r = _optional(residual, "residual", _BF16, (T, H), device)
     guard, st = _launch(device, stream)
     with guard:
-        y = _output(out, "out", _BF16, (T, H), device)
+        y = _output(out, "out", x, (T, H), device)
         s, sp = x, None
         if residual is not None:
-            s = _output(residual_out, "residual_out", _BF16, (T, H), device)
+            s = _output(residual_out, "residual_out", x, (T, H), device)
             sp = s.data_ptr()
         elif residual_out is not None:
             raise ValueError("residual_out was given without a residual")
@@ -139,8 +140,8 @@ def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, wor
     dr = _optional(dresidual, "dresidual", _BF16, (T, H), device)
     guard, st = _launch(device, stream)
     with guard:
-        dx = _output(dx, "dx", _BF16, (T, H), device)
-        dw = _output(dw, "dw", _BF16, (H,), device)
+        dx = _output(dx, "dx", dy, (T, H), device)
+        dw = _output(dw, "dw", weight, (H,), device)
         L = lib()
         ws = _workspace(workspace, L.moe_rms_norm_backward_workspace_size(T, H), device)
         _check(L.moe_rms_norm_backward(dy.data_ptr(), sp, w, r, dr, T, H, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
@@ -166,7 +167,7 @@ def gated_ffn(x, w_gate_up, act: str = "silu", save: bool = False, out=None, str
     I, w = _gate_up_sizes(w_gate_up, H, device)
     guard, st = _launch(device, stream)
     with guard:
-        h = _output(out, "out", _BF16, (T, I), device)
+        h = _output(out, "out", x, (T, I), device)
         gu = torch.empty((T, 2 * I), dtype=_F32, device=device) if save else None
         _check(lib().moe_gated_ffn(x.data_ptr(), w, T, H, I, a, h.data_ptr(), gu.data_ptr() if save else None, st),
                "moe_gated_ffn")
@@ -183,8 +184,8 @@ def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None
     g = _tensor(gu, "gu", _F32, (T, 2 * I), device)
     guard, st = _launch(device, stream)
     with guard:
-        dx = _output(dx, "dx", _BF16, (T, H), device)
-        dw = _output(dw, "dw", _BF16, (2 * I, H), device)
+        dx = _output(dx, "dx", x, (T, H), device)
+        dw = _output(dw, "dw", w_gate_up, (2 * I, H), device)
         L = lib()
         ws = _workspace(workspace, L.moe_gated_ffn_backward_workspace_size(T, I), device)
         _check(L.moe_gated_ffn_backward(d, x.data_ptr(), w, g, T, H, I, a, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
@@ -206,7 +207,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False
     r = _optional(residual, "residual", _BF16, (T, N), device)
     guard, st = _launch(device, stream)
     with guard:
-        y = _output(out, "out", _BF16, (T, N), device)
+        y = _output(out, "out", x, (T, N), device)
         z = torch.empty((T, N), dtype=_F32, device=device) if save and act != "none" else None
         _check(lib().moe_linear(x.data_ptr(), wp, b, r, T, K, N, a, y.data_ptr(),
                                 None if z is None else z.data_ptr(), st), "moe_linear")
@@ -227,8 +228,8 @@ def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=
     zp = _optional(z, "z", _F32, (T, N), device)
     guard, st = _launch(device, stream)
     with guard:
-        dx = _output(dx, "dx", _BF16, (T, K), device)
-        dw = _output(dw, "dw", _BF16, (N, K), device)
+        dx = _output(dx, "dx", x, (T, K), device)
+        dw = _output(dw, "dw", w, (N, K), device)
         db = torch.empty((N,), dtype=_BF16, device=device) if bias else None
         L = lib()
         ws = _workspace(workspace, L.moe_linear_backward_workspace_size(T, N, a, int(bool(bias))), device)

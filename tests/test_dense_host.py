@@ -65,7 +65,7 @@ def test_norm_backward_refusals(L):
     assert call(L.moe_rms_norm_backward, a, bytes=a["bytes"] - 1) == SPACE
     assert L.moe_rms_norm_backward_workspace_size(4, 100) == 0
     assert L.moe_rms_norm_backward_workspace_size(-1, 256) == 0
-    # one fp32 row for each of at most 296 row classes
+    # one fp32 row for each block of the first pass: two of 512 threads on each of 148 SMs
     assert L.moe_rms_norm_backward_workspace_size(10 ** 6, 4096) == 296 * 4096 * 4
 
 

@@ -24,7 +24,11 @@ NORM_SIZES = [(1, 2048), (1, 8), (3, 64), (129, 128), (5, 1024), (7, 1032), (33,
               (301, 8192), (3, 8200), (2, 16384), (2, 32776), (1, 65536)]
 
 
-@pytest.mark.parametrize("T,H", NORM_SIZES)
+# batches whose rows outnumber the blocks, at widths with 1, 2 and 4 vectors a thread
+NORM_MANY = [(1500, 1032), (2500, 2048), (1000, 4096), (1203, 4104), (700, 7168), (801, 8192), (611, 8200), (500, 16384)]
+
+
+@pytest.mark.parametrize("T,H", NORM_SIZES + NORM_MANY)
 @pytest.mark.parametrize("residual", [False, True])
 def test_rms_norm(T, H, residual):
     x, w = normal(T + H, T, H), normal(H, H, std=0.2, mean=1.0)
@@ -36,7 +40,8 @@ def test_rms_norm(T, H, residual):
     R.check(n.y, y, (R.HALF + 2 * R.NORM) * y.abs(), "y")
 
 
-@pytest.mark.parametrize("T,H", [(1, 128), (16, 2048), (77, 7168), (3, 1152), (130, 4096), (1, 65536)])
+@pytest.mark.parametrize("T,H", [(1, 128), (16, 2048), (77, 7168), (3, 1152), (130, 4096), (1, 65536),
+                                 (2500, 2048), (700, 7168), (500, 16384)])
 def test_rms_norm_codes(T, H):
     x, w, r = normal(1, T, H), normal(2, H, std=0.2, mean=1.0), normal(3, T, H)
     x[0, :128] = 0
@@ -54,6 +59,15 @@ def test_rms_norm_codes(T, H):
     got = n.codes.float().view(T, H // 128, 128).double() * n.scales.double()[:, :, None]
     bound = (2.0 ** -4 + 4 * R.NORM) * g.abs() + 2.0 ** -10 * ref[:, :, None] * (1 + 4 * R.NORM)
     R.check(got, g, bound, "codes")
+
+
+@pytest.mark.parametrize("H", [512, 2048, 7168, 8192, 16384])
+def test_rms_norm_rows_do_not_depend_on_the_batch(H):
+    """A row's result is the same bits alone and among many rows."""
+    x, r, w = normal(1, 1000, H), normal(2, 1000, H), normal(3, H, mean=1.0)
+    many = moe.rms_norm(x, w, residual=r, rstd=True)
+    few = moe.rms_norm(x[990:993].contiguous(), w, residual=r[990:993].contiguous(), rstd=True)
+    assert torch.equal(few.y, many.y[990:993]) and torch.equal(few.rstd, many.rstd[990:993])
 
 
 def test_rms_norm_small_and_large_rows():
@@ -84,7 +98,7 @@ def test_rms_norm_in_place():
 
 
 @pytest.mark.parametrize("T,H", [(1, 8), (1, 2048), (2, 64), (297, 512), (700, 2040), (64, 4096), (33, 7168), (3, 8200),
-                                 (1000, 2048), (5, 16384), (3, 65536)])
+                                 (1000, 2048), (5, 16384), (3, 65536)] + NORM_MANY)
 @pytest.mark.parametrize("residual", [False, True])
 def test_rms_norm_backward(T, H, residual):
     s, w, dy = normal(T, T, H, std=1.5), normal(H, H, std=0.2, mean=1.0), normal(T + 1, T, H, std=0.1)
