@@ -67,18 +67,6 @@ __device__ __forceinline__ void tile_coord(int tile, int m_tiles, int n_tiles, i
   m = g * kGroupM + (r - n * gm);
 }
 
-// acc = act(acc) for the 32 columns in registers
-template <int kAct>
-__device__ __forceinline__ void act32(float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_t<kAct>(v[i]);
-}
-template <int kAct>
-__device__ __forceinline__ void gate32(float (&g)[32], const float (&u)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) g[i] = gated_act_t<kAct>(g[i], u[i]);
-}
-
 // The warp's two staging buffers and the TMA stores out of them.
 struct Stager {
   uint8_t* base;
@@ -323,15 +311,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
       const int y0 = (mt * TL::kCtas + rank) * kTileM + quad * 32;
       const int x0 = nt * kOutN + half * kCols;
+      const bool rows = y0 < p.M;
+      const bool mine = y0 + lane < p.M;
+      // the residual of the first columns is on its way while the tile's MMAs run
+      const __nv_bfloat16* res =
+          !kGated && p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * p.N : nullptr;
+      uint4 rv[4];
+      auto load_res = [&](int x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          rv[i] = res != nullptr && x + 8 * i < p.N ? *reinterpret_cast<const uint4*>(res + x + 8 * i)
+                                                    : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (!kGated) load_res(x0);
       const bool got = mbar_wait_bounded(&tfull[acc], aph, s_abort, s_status, p.timeout_ns);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                           static_cast<uint32_t>(acc * kBN + half * kCols);
-      const bool rows = y0 < p.M;
-      const bool mine = y0 + lane < p.M;
-      const __nv_bfloat16* res =
-          p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * p.N : nullptr;
 #pragma unroll 1
       for (int c = 0; c < kCols; c += 32) {
         const int x = x0 + c;
@@ -344,18 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             st.store_f32(&tmS0, v, x, y0, p.N, rows);
             st.store_f32(&tmS1, u, x, y0, p.N, rows);
           }
-          if (p.act == MOE_ACT_SILU)
-            gate32<MOE_ACT_SILU>(v, u);
-          else if (p.act == MOE_ACT_GELU)
-            gate32<MOE_ACT_GELU>(v, u);
-          else
-            gate32<MOE_ACT_RELU>(v, u);
-        } else {
-          uint4 rv[4];
+          with_act(p.act, [&](auto tag) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            rv[i] = res != nullptr && x + 8 * i < p.N ? *reinterpret_cast<const uint4*>(res + x + 8 * i)
-                                                      : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 32; ++i) v[i] = act_t<decltype(tag)::value>(v[i]) * u[i];
+          });
+        } else {
           tmem_load32(tb + c, v);
           if (p.bias != nullptr) {
 #pragma unroll
@@ -371,12 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (p.save) st.store_f32(&tmS0, v, x, y0, p.N, rows);
-          if (p.act == MOE_ACT_SILU)
-            act32<MOE_ACT_SILU>(v);
-          else if (p.act == MOE_ACT_GELU)
-            act32<MOE_ACT_GELU>(v);
-          else if (p.act == MOE_ACT_RELU)
-            act32<MOE_ACT_RELU>(v);
+          if (p.act != kActNone) {
+            with_act(p.act, [&](auto tag) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = act_t<decltype(tag)::value>(v[i]);
+            });
+          }
           if (p.residual != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -387,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v[8 * i + 2 * q + 1] += bf16_hi(w[q]);
               }
             }
+            if (c + 32 < kCols) load_res(x + 32);
           }
         }
         st.store_bf16(&tmY, v, x, y0, rows && x < p.N);
@@ -494,18 +485,22 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmY, tmS0, tmS1, p);
 }
 
-// Tile choice: the shape with the least estimated time, waves x (K steps x
-// cycles a step + tile overhead).
+// Tile choice: the shape with the least estimated time, waves x (K steps x a
+// step + a tile's overhead). Measured on B200 with all SMs at work, a K step of 64
+// takes 0.34-0.38 us for 256 x 256 on a pair and 0.40-0.45 for 128 x 256 (a third
+// more bytes through shared memory), but still 0.28-0.31 at 128 columns: there the
+// issuing thread's own path (wait, four MMAs, commit) is as long as the MMAs of
+// 256 columns. So the narrow tiles only pay where they save a wave.
 template <bool kAmn, bool kBmn, bool kGated>
 cudaError_t launch_order(const DenseGemm& g, int num_sms, cudaStream_t st) {
   const long long kb = (g.K + kBK - 1) / kBK;
   auto cost = [&](int rows, int cols, int slots, int per_step) {
     const int outn = kGated ? cols / 2 : cols;
     const long long tiles = ((g.M + rows - 1ll) / rows) * ((g.N + outn - 1ll) / outn);
-    return ((tiles + slots - 1) / slots) * (kb * per_step + 1000);
+    return ((tiles + slots - 1) / slots) * (kb * per_step + 1500);
   };
-  const long long c[4] = {cost(256, 256, num_sms / 2, 560), cost(256, 128, num_sms / 2, 340),
-                          cost(128, 256, num_sms, 640), cost(128, 128, num_sms, 400)};
+  const long long c[4] = {cost(256, 256, num_sms / 2, 347), cost(256, 128, num_sms / 2, 300),
+                          cost(128, 256, num_sms, 410), cost(128, 128, num_sms, 290)};
   int best = 0;
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[best]) best = i;

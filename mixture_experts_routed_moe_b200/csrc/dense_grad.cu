@@ -15,9 +15,12 @@
 namespace moe {
 namespace {
 
+constexpr int kGradCols = 128;  // columns of a block of linear_grad_kernel
+
+template <int kAct>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict__ gu,
                                                          const __nv_bfloat16* __restrict__ dh,
-                                                         __nv_bfloat16* __restrict__ dgu, long long T, int I, int act) {
+                                                         __nv_bfloat16* __restrict__ dgu, long long T, int I) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
   const int nv = I / 8;
@@ -37,8 +40,8 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       float f0, s0, f1, s1;
-      act_and_slope(act, g[2 * q], f0, s0);
-      act_and_slope(act, g[2 * q + 1], f1, s1);
+      act_and_slope<kAct>(g[2 * q], f0, s0);
+      act_and_slope<kAct>(g[2 * q + 1], f1, s1);
       const float a = bf16_lo(dw[q]), b = bf16_hi(dw[q]);
       og[q] = pack_bf16x2(a * u[2 * q] * s0, b * u[2 * q + 1] * s1);
       ou[q] = pack_bf16x2(a * f0, b * f1);
@@ -48,57 +51,60 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict
   }
 }
 
-// Block (x, y): 256 columns (8 per lane of a warp), rows y, y + 8, ... by its
-// eight warps within the row range of blockIdx.y; dz written, the fp32 column
-// sums of the range added over the warps in order and left in partial[y].
-__global__ void __launch_bounds__(256) linear_grad_kernel(const float* __restrict__ z,
+// Block (x, y): 128 columns (4 a lane of a warp), rows y, y + 8, ... by its
+// eight warps within the row range of blockIdx.y, four rows' loads in flight; dz
+// written, the fp32 column sums of the range added over the warps in order and
+// left in partial[y].
+template <int kAct>
+__global__ void __launch_bounds__(256, 4) linear_grad_kernel(const float* __restrict__ z,
                                                           const __nv_bfloat16* __restrict__ dy,
                                                           __nv_bfloat16* __restrict__ dz, float* __restrict__ partial,
-                                                          long long T, int N, int act) {
+                                                          long long T, int N) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_sum[8][257];
+  constexpr int kRows = 4;
+  __shared__ float s_sum[8][kGradCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lane * 8;
+  const int c = blockIdx.x * kGradCols + lane * 4;
   const long long t0 = blockIdx.y * T / gridDim.y, t1 = (blockIdx.y + 1) * T / gridDim.y;
-  float sum[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) sum[q] = 0.f;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < N) {
-#pragma unroll 2
-    for (long long t = t0 + warp; t < t1; t += 8) {
-      const size_t at = static_cast<size_t>(t) * N + c;
-      const uint4 d = *reinterpret_cast<const uint4*>(dy + at);
-      const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
-      float v[8];
+    for (long long t = t0 + warp; t < t1; t += 8 * kRows) {
+      uint2 d[kRows];
+      float4 zz[kRows];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[2 * q] = bf16_lo(dw[q]);
-        v[2 * q + 1] = bf16_hi(dw[q]);
+      for (int k = 0; k < kRows; ++k) {
+        const size_t at = static_cast<size_t>(t + 8 * k) * N + c;
+        d[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint2*>(dy + at) : make_uint2(0u, 0u);
+        if (kAct != kActNone)
+          zz[k] = t + 8 * k < t1 ? *reinterpret_cast<const float4*>(z + at) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      if (act != kActNone) {
-        const float4* zp = reinterpret_cast<const float4*>(z + at);
-        const float4 z0 = zp[0], z1 = zp[1];
-        const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float f, s;
-          act_and_slope(act, zz[q], f, s);
-          v[q] *= s;
+      for (int k = 0; k < kRows; ++k) {
+        float v[4] = {bf16_lo(d[k].x), bf16_hi(d[k].x), bf16_lo(d[k].y), bf16_hi(d[k].y)};
+        if (kAct != kActNone) {
+          const float zk[4] = {zz[k].x, zz[k].y, zz[k].z, zz[k].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float f, s;
+            act_and_slope<kAct>(zk[q], f, s);
+            v[q] *= s;
+          }
+          if (t + 8 * k < t1)
+            *reinterpret_cast<uint2*>(dz + static_cast<size_t>(t + 8 * k) * N + c) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         }
-        *reinterpret_cast<uint4*>(dz + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                        pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) sum[q] += v[q];
+        for (int q = 0; q < 4; ++q) sum[q] += v[q];
+      }
     }
   }
   if (partial == nullptr) return;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) s_sum[warp][lane * 8 + q] = sum[q];
+  for (int q = 0; q < 4; ++q) s_sum[warp][lane * 4 + q] = sum[q];
   __syncthreads();
-  const int col = blockIdx.x * 256 + threadIdx.x;
-  if (col < N) {
+  const int col = blockIdx.x * kGradCols + threadIdx.x;
+  if (threadIdx.x < kGradCols && col < N) {
     float t = s_sum[0][threadIdx.x];
 #pragma unroll
     for (int w = 1; w < 8; ++w) t += s_sum[w][threadIdx.x];
@@ -112,24 +118,28 @@ cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T,
                               cudaStream_t st) {
   const long long n = static_cast<long long>(T) * (I / 8);
   const long long blocks = std::min<long long>((n + 255) / 256, static_cast<long long>(num_sms) * 8);
-  return launch_pdl(gated_grad_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, gu,
-                    static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dgu),
-                    static_cast<long long>(T), I, act);
+  return with_act(act, [&](auto tag) {
+    return launch_pdl(gated_grad_kernel<decltype(tag)::value>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
+                      gu, static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dgu),
+                      static_cast<long long>(T), I);
+  });
 }
 
 int linear_grad_rows(int T, int N) {
-  // row ranges: enough blocks for the device, at least 32 rows each
-  const int cols = (N + 255) / 256;
-  return std::max(1, std::min((T + 31) / 32, (1184 + cols - 1) / cols));
+  // row ranges: one wave of four blocks an SM of a B200, at least 64 rows each
+  const int cols = (N + kGradCols - 1) / kGradCols;
+  return std::max(1, std::min((T + 63) / 64, std::max(1, 592 / cols)));
 }
 
 cudaError_t launch_linear_grad(const float* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
                                int act, cudaStream_t st) {
   const int rows = linear_grad_rows(T, N);
-  cudaError_t err = launch_pdl(linear_grad_kernel, dim3(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(rows)),
-                               dim3(256), 0, st, z, static_cast<const __nv_bfloat16*>(dy),
-                               static_cast<__nv_bfloat16*>(dz), db != nullptr ? partial : static_cast<float*>(nullptr),
-                               static_cast<long long>(T), N, act);
+  const dim3 grid(static_cast<unsigned>((N + kGradCols - 1) / kGradCols), static_cast<unsigned>(rows));
+  const cudaError_t err = with_act(act, [&](auto tag) {
+    return launch_pdl(linear_grad_kernel<decltype(tag)::value>, grid, dim3(256), 0, st, z,
+                      static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dz),
+                      db != nullptr ? partial : static_cast<float*>(nullptr), static_cast<long long>(T), N);
+  });
   if (err != cudaSuccess || db == nullptr) return err;
   return launch_column_sum(partial, rows, N, db, st);
 }

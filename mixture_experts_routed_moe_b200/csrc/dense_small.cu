@@ -66,10 +66,6 @@ __device__ __forceinline__ float4 sum_ranks(uint32_t addr) {
   return v[0];
 }
 
-__device__ __forceinline__ float act_any(int act, float z) {
-  return act == kActNone ? z : gated_act(act, z, 1.0f);
-}
-
 // This CTA's share of the unit's outputs, four consecutive ones of a token per step.
 template <bool kGated, int kC>
 __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int rank, bool aborted) {
@@ -92,10 +88,13 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
         *reinterpret_cast<float4*>(s) = g;
         *reinterpret_cast<float4*>(s + p.N) = u;
       }
-      v[0] = gated_act(p.act, g.x, u.x);
-      v[1] = gated_act(p.act, g.y, u.y);
-      v[2] = gated_act(p.act, g.z, u.z);
-      v[3] = gated_act(p.act, g.w, u.w);
+      with_act(p.act, [&](auto tag) {
+        constexpr int kAct = decltype(tag)::value;
+        v[0] = act_t<kAct>(g.x) * u.x;
+        v[1] = act_t<kAct>(g.y) * u.y;
+        v[2] = act_t<kAct>(g.z) * u.z;
+        v[3] = act_t<kAct>(g.w) * u.w;
+      });
     } else {
       uint2 res = make_uint2(0u, 0u);
       if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + at);
@@ -108,10 +107,13 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
         z.w += bf16_hi(b.y);
       }
       if (p.save != nullptr) *reinterpret_cast<float4*>(p.save + at) = z;
-      v[0] = act_any(p.act, z.x);
-      v[1] = act_any(p.act, z.y);
-      v[2] = act_any(p.act, z.z);
-      v[3] = act_any(p.act, z.w);
+      with_act(p.act, [&](auto tag) {
+        constexpr int kAct = decltype(tag)::value;
+        v[0] = act_t<kAct>(z.x);
+        v[1] = act_t<kAct>(z.y);
+        v[2] = act_t<kAct>(z.z);
+        v[3] = act_t<kAct>(z.w);
+      });
       if (p.residual != nullptr) {
         v[0] += bf16_lo(res.x);
         v[1] += bf16_hi(res.x);
