@@ -53,33 +53,31 @@ cudaError_t run(const DenseGemm& g, int sms, cudaStream_t st) {
   return dense_small_supported(g) ? launch_dense_small(g, sms, st) : launch_dense_gemm(g, sms, st);
 }
 
-// dx = d W (d [T, M], W [M, K]) and dw = d^T x; either may be null
+// dx = d W (d [T, M], W [M, K]) and dw = d^T x; either may be null. Few tokens'
+// dx streams the weights; else both products share one launch.
 cudaError_t backward_products(const void* d, const void* x, const void* w, int T, int M, int K, void* dx, void* dw,
                               int sms, cudaStream_t st) {
+  DenseGemm gx{}, gw{};
+  gx.order = kLinearNN;
+  gx.M = T;
+  gx.N = K;
+  gx.K = M;
+  gx.a = d;
+  gx.b = w;
+  gx.out = dx;
+  gw.order = kLinearTN;
+  gw.M = M;
+  gw.N = K;
+  gw.K = T;
+  gw.a = d;
+  gw.b = x;
+  gw.out = dw;
+  if (dx != nullptr && dw != nullptr && !dense_small_supported(gx)) return launch_dense_gemm_backward(gx, gw, sms, st);
   if (dx != nullptr) {
-    DenseGemm g{};
-    g.order = kLinearNN;
-    g.M = T;
-    g.N = K;
-    g.K = M;
-    g.a = d;
-    g.b = w;
-    g.out = dx;
-    const cudaError_t err = run(g, sms, st);
+    const cudaError_t err = run(gx, sms, st);
     if (err != cudaSuccess) return err;
   }
-  if (dw != nullptr) {
-    DenseGemm g{};
-    g.order = kLinearTN;
-    g.M = M;
-    g.N = K;
-    g.K = T;
-    g.a = d;
-    g.b = x;
-    g.out = dw;
-    return run(g, sms, st);
-  }
-  return cudaSuccess;
+  return dw != nullptr ? launch_dense_gemm(gw, sms, st) : cudaSuccess;
 }
 
 }  // namespace

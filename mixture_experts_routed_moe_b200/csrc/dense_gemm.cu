@@ -4,9 +4,14 @@
 //   linear:  out[m, n] = bf16(act(sum_k A[m,k] B[n,k] + bias[n]) + residual[m, n])
 //   gated:   out[m, n] = bf16(act(sum_k A[m,k] B[n,k]) * sum_k A[m,k] B[N+n,k])
 // optionally keeping the fp32 pre-activations (linear z[m,n]; gated g and u)
-// for the backward pass. The products of the backward pass are linear ones
-// with other operand orders: dx = dz W reads W as an MN-major B, and
-// dW = dz^T x reads both operands MN-major, so nothing is transposed in memory.
+// for the backward pass. The products of the backward pass run in one launch:
+//   dx = d W       A = d K-major, B = W MN-major
+//   dW = d^T x     both MN-major
+// Nothing is transposed in memory, and the tiles of both products share the
+// waves: the longer ones first, the workers taking tiles in turn, so that one
+// product's last wave is filled by the other's tiles (T = 4096, 2I = 2816, H =
+// 2048: 88 tiles of 64 K steps and 128 of 44 on 74 pairs take 172 steps; one
+// after the other, 128 + 88).
 //
 // Tiles: a pair (cta_group::2) computes 256 x kBN, a single CTA 128 x kBN; the
 // gated form takes kBN/2 gate and kBN/2 up rows of B for one tile (in a pair
@@ -36,15 +41,27 @@ constexpr int kBox = 32 * 64;  // a staging buffer: 32 rows of 64 bytes
 constexpr int kStaging = kEpiWarps * 2 * kBox;
 constexpr int kGroupM = 8;  // row blocks that are walked together along the columns (their A and B tiles meet in L2)
 
+enum Mode { kModeGated, kModeLinear, kModeBackward };
+
+// One product: out [M, N] over num_kb K steps, in m_tiles x n_tiles tiles.
+struct Product {
+  int M, N, num_kb, m_tiles, n_tiles;
+  int a_mn;  // the A operand is MN-major (backward mode)
+  __nv_bfloat16* out;
+};
+
 struct GemmParams {
-  int M, N;  // of the output
-  int num_kb, m_tiles, n_tiles;
+  Product prod[2];  // the second only in backward mode
+  int first_tiles, tiles;  // tiles of the first product, of both
   int act, save, stall;
-  int up_row;  // gated: first up row of B
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
-  __nv_bfloat16* out;
   unsigned long long timeout_ns;
+};
+
+// Tensor maps of the products' operands and outputs; save: fp32 z, or g and u.
+struct GemmMaps {
+  CUtensorMap a[2], b[2], y[2], save[2];
 };
 
 template <bool kPair, int kBN>
@@ -58,13 +75,22 @@ struct Tile {
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kStaging + (2 * kStages + 5) * 8 + 16;
 };
 
-__device__ __forceinline__ void tile_coord(int tile, int m_tiles, int n_tiles, int& m, int& n) {
-  const int per = kGroupM * n_tiles;
+struct Coord {
+  int prob, m, n;
+};
+template <int kMode>
+__device__ __forceinline__ Coord tile_coord(const GemmParams& p, int tile) {
+  Coord c;
+  c.prob = kMode == kModeBackward && tile >= p.first_tiles ? 1 : 0;
+  if (c.prob) tile -= p.first_tiles;
+  const int m_tiles = p.prod[c.prob].m_tiles;
+  const int per = kGroupM * p.prod[c.prob].n_tiles;
   const int g = tile / per;
   const int gm = min(kGroupM, m_tiles - g * kGroupM);
   const int r = tile - g * per;
-  n = r / gm;
-  m = g * kGroupM + (r - n * gm);
+  c.n = r / gm;
+  c.m = g * kGroupM + (r - c.n * gm);
+  return c;
 }
 
 // The warp's two staging buffers and the TMA stores out of them.
@@ -120,12 +146,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-template <bool kPair, int kBN, bool kAmn, bool kBmn, bool kGated>
+template <bool kPair, int kBN, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-    dense_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmS0,
-                      const __grid_constant__ CUtensorMap tmS1, const GemmParams p) {
+    dense_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p) {
   using TL = Tile<kPair, kBN>;
+  constexpr bool kGated = kMode == kModeGated;
+  constexpr bool kBmn = kMode == kModeBackward;
   constexpr int kStages = TL::kStages;
   constexpr int kOutN = kGated ? kBN / 2 : kBN;
   extern __shared__ uint8_t smem_raw[];
@@ -160,9 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbarrier_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
-    prefetch_tensormap(&tmY);
+    prefetch_tensormap(&maps.a[0]);
+    prefetch_tensormap(&maps.b[0]);
+    prefetch_tensormap(&maps.y[0]);
   }
   if (warp == 1) {
     if (kPair) {
@@ -180,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *s_tmem;
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
-  const int total = p.m_tiles * p.n_tiles;
+  const int total = p.tiles;
   const int worker = blockIdx.x / TL::kCtas, nworkers = gridDim.x / TL::kCtas;
 
   if (warp == 0) {
@@ -190,10 +216,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = worker; ok && tile < total; tile += nworkers) {
-        int mt, nt;
-        tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
-        const int m0 = (mt * TL::kCtas + rank) * kTileM;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        const Coord c = tile_coord<kMode>(p, tile);
+        const int num_kb = p.prod[c.prob].num_kb;
+        const bool a_mn = kMode == kModeBackward && p.prod[c.prob].a_mn;
+        const CUtensorMap* tmA = &maps.a[c.prob];
+        const CUtensorMap* tmB = &maps.b[c.prob];
+        const int up_row = p.prod[0].N;  // gated: the first up row of B
+        const int m0 = (c.m * TL::kCtas + rank) * kTileM;
+        for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) {
             ok = false;
             break;
@@ -208,25 +238,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* a = sA + stage * TL::kA;
           uint8_t* b = sB + stage * TL::kB;
           const int k0 = kb * kBK;
-          if (kAmn) {
-            load(a, &tmA, m0, k0);
-            load(a + 8192, &tmA, m0 + 64, k0);
+          if (a_mn) {
+            load(a, tmA, m0, k0);
+            load(a + 8192, tmA, m0 + 64, k0);
           } else {
-            load(a, &tmA, k0, m0);
+            load(a, tmA, k0, m0);
           }
           if (kGated) {
             if (kPair) {
-              load(b, &tmB, k0, nt * kOutN + rank * p.up_row);
+              load(b, tmB, k0, c.n * kOutN + rank * up_row);
             } else {
-              load(b, &tmB, k0, nt * kOutN);
-              load(b + TL::kB / 2, &tmB, k0, nt * kOutN + p.up_row);
+              load(b, tmB, k0, c.n * kOutN);
+              load(b + TL::kB / 2, tmB, k0, c.n * kOutN + up_row);
             }
           } else if (kBmn) {
 #pragma unroll
             for (int j = 0; j < TL::kBRows / 64; ++j)
-              load(b + j * 8192, &tmB, nt * kBN + rank * TL::kBRows + 64 * j, k0);
+              load(b + j * 8192, tmB, c.n * kBN + rank * TL::kBRows + 64 * j, k0);
           } else {
-            load(b, &tmB, k0, nt * kBN + rank * TL::kBRows);
+            load(b, tmB, k0, c.n * kBN + rank * TL::kBRows);
           }
           if (++stage == kStages) {
             stage = 0;
@@ -249,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idesc = idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, kAmn, kBmn);
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
@@ -257,7 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, s_abort, s_status, p.timeout_ns)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        const int prob = kMode == kModeBackward && tile >= p.first_tiles ? 1 : 0;
+        const int num_kb = p.prod[prob].num_kb;
+        const bool a_mn = kMode == kModeBackward && p.prod[prob].a_mn;
+        const uint32_t idesc = a_mn ? idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, true, kBmn)
+                                    : idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, false, kBmn);
+        for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait_bounded(&full[stage], ph, s_abort, s_status, p.timeout_ns)) {
             ok = false;
             break;
@@ -267,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b0 = smem_u32(sB + stage * TL::kB);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t da = kAmn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32);
+            const uint64_t da = a_mn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32);
             const uint64_t db = kBmn ? sdesc_mnmajor_sw128(b0 + k * 2048) : sdesc_kmajor_sw128(b0 + k * 32);
             if (kPair)
               umma_bf16_pair(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
@@ -307,23 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t aph = 0;
     int tile = worker;
     for (; tile < total; tile += nworkers) {
-      int mt, nt;
-      tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
-      const int y0 = (mt * TL::kCtas + rank) * kTileM + quad * 32;
-      const int x0 = nt * kOutN + half * kCols;
-      const bool rows = y0 < p.M;
-      const bool mine = y0 + lane < p.M;
+      const Coord co = tile_coord<kMode>(p, tile);
+      const int M = p.prod[co.prob].M, N = p.prod[co.prob].N;
+      const CUtensorMap* tmY = &maps.y[co.prob];
+      const int y0 = (co.m * TL::kCtas + rank) * kTileM + quad * 32;
+      const int x0 = co.n * kOutN + half * kCols;
+      const bool rows = y0 < M;
+      const bool mine = y0 + lane < M;
       // the residual of the first columns is on its way while the tile's MMAs run
       const __nv_bfloat16* res =
-          !kGated && p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * p.N : nullptr;
+          kMode == kModeLinear && p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * N : nullptr;
       uint4 rv[4];
       auto load_res = [&](int x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          rv[i] = res != nullptr && x + 8 * i < p.N ? *reinterpret_cast<const uint4*>(res + x + 8 * i)
+          rv[i] = res != nullptr && x + 8 * i < N ? *reinterpret_cast<const uint4*>(res + x + 8 * i)
                                                     : make_uint4(0u, 0u, 0u, 0u);
       };
-      if (!kGated) load_res(x0);
+      if (kMode == kModeLinear) load_res(x0);
       const bool got = mbar_wait_bounded(&tfull[acc], aph, s_abort, s_status, p.timeout_ns);
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
@@ -338,19 +373,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_load32(tb + c, v);
           tmem_load32(tb + kOutN + c, u);
           if (p.save) {
-            st.store_f32(&tmS0, v, x, y0, p.N, rows);
-            st.store_f32(&tmS1, u, x, y0, p.N, rows);
+            st.store_f32(&maps.save[0], v, x, y0, N, rows);
+            st.store_f32(&maps.save[1], u, x, y0, N, rows);
           }
           with_act(p.act, [&](auto tag) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = act_t<decltype(tag)::value>(v[i]) * u[i];
           });
+        } else if (kMode == kModeBackward) {
+          tmem_load32(tb + c, v);
         } else {
           tmem_load32(tb + c, v);
           if (p.bias != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (x + 8 * i >= p.N) continue;
+              if (x + 8 * i >= N) continue;
               const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + x + 8 * i));
               const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -360,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (p.save) st.store_f32(&tmS0, v, x, y0, p.N, rows);
+          if (p.save) st.store_f32(&maps.save[0], v, x, y0, N, rows);
           if (p.act != kActNone) {
             with_act(p.act, [&](auto tag) {
 #pragma unroll
@@ -380,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + 32 < kCols) load_res(x + 32);
           }
         }
-        st.store_bf16(&tmY, v, x, y0, rows && x < p.N);
+        st.store_bf16(tmY, v, x, y0, rows && x < N);
       }
       tc_fence_before();
       __syncwarp();
@@ -395,13 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // a wait gave up (never in normal operation): mark what this warp did not compute
     for (; tile < total; tile += nworkers) {
-      int mt, nt;
-      tile_coord(tile, p.m_tiles, p.n_tiles, mt, nt);
-      const int y = (mt * TL::kCtas + rank) * kTileM + quad * 32 + lane;
-      const int x0 = nt * kOutN + half * kCols;
-      if (y < p.M)
-        for (int x = x0; x < min(x0 + kCols, p.N); ++x)
-          p.out[static_cast<size_t>(y) * p.N + x] = __ushort_as_bfloat16(0x7FC0);
+      const Coord co = tile_coord<kMode>(p, tile);
+      const Product& pr = p.prod[co.prob];
+      const int y = (co.m * TL::kCtas + rank) * kTileM + quad * 32 + lane;
+      const int x0 = co.n * kOutN + half * kCols;
+      if (y < pr.M)
+        for (int x = x0; x < min(x0 + kCols, pr.N); ++x)
+          pr.out[static_cast<size_t>(y) * pr.N + x] = __ushort_as_bfloat16(0x7FC0);
     }
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
@@ -417,52 +454,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kPair, int kBN, bool kAmn, bool kBmn, bool kGated>
-cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
+template <bool kPair, int kBN, int kMode>
+cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
   using TL = Tile<kPair, kBN>;
+  constexpr bool kGated = kMode == kModeGated;
   constexpr int kOutN = kGated ? kBN / 2 : kBN;
-  GemmParams p{};
-  p.M = g.M;
-  p.N = g.N;
-  p.num_kb = (g.K + kBK - 1) / kBK;
-  p.m_tiles = (g.M + kTileM * TL::kCtas - 1) / (kTileM * TL::kCtas);
-  p.n_tiles = (g.N + kOutN - 1) / kOutN;
-  if (static_cast<long long>(p.m_tiles) * p.n_tiles >= (1ll << 31)) return cudaErrorInvalidValue;
-  p.act = g.act;
-  p.save = g.save0 != nullptr;
-  p.stall = stall_gate_up_loads();
-  p.up_row = g.N;
-  p.bias = static_cast<const __nv_bfloat16*>(g.bias);
-  p.residual = static_cast<const __nv_bfloat16*>(g.residual);
-  p.out = static_cast<__nv_bfloat16*>(g.out);
-  p.timeout_ns = wait_limit_ns();
-
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const uint64_t b_rows = kGated ? 2 * static_cast<uint64_t>(g.N) : g.N;
-  CUtensorMap tmA, tmB, tmY, tmS0, tmS1;
-  bool ok = kAmn ? encode_tensor_map_2d(&tmA, bf16, 2, g.a, g.M, g.K, 64, kBK)
-                 : encode_tensor_map_2d(&tmA, bf16, 2, g.a, g.K, g.M, kBK, kTileM);
-  ok = ok && (kBmn ? encode_tensor_map_2d(&tmB, bf16, 2, g.b, g.N, g.K, 64, kBK)
-                   : encode_tensor_map_2d(&tmB, bf16, 2, g.b, g.K, b_rows, kBK,
-                                          kGated ? kOutN : TL::kBRows));
-  ok = ok && encode_tensor_map_2d(&tmY, bf16, 2, g.out, g.N, g.M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-  if (!ok) return cudaErrorInvalidValue;
-  tmS0 = tmS1 = tmY;
+  GemmParams p{};
+  GemmMaps maps;
+  long long tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    Product& q = p.prod[i];
+    q.M = g[i].M;
+    q.N = g[i].N;
+    q.num_kb = (g[i].K + kBK - 1) / kBK;
+    q.m_tiles = (q.M + kTileM * TL::kCtas - 1) / (kTileM * TL::kCtas);
+    q.n_tiles = (q.N + kOutN - 1) / kOutN;
+    q.a_mn = g[i].order == kLinearTN;
+    q.out = static_cast<__nv_bfloat16*>(g[i].out);
+    tiles += static_cast<long long>(q.m_tiles) * q.n_tiles;
+    if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+    if (i == 0) p.first_tiles = static_cast<int>(tiles);
+    bool ok = q.a_mn ? encode_tensor_map_2d(&maps.a[i], bf16, 2, g[i].a, g[i].M, g[i].K, 64, kBK)
+                     : encode_tensor_map_2d(&maps.a[i], bf16, 2, g[i].a, g[i].K, g[i].M, kBK, kTileM);
+    ok = ok && (kMode == kModeBackward
+                    ? encode_tensor_map_2d(&maps.b[i], bf16, 2, g[i].b, g[i].N, g[i].K, 64, kBK)
+                    : encode_tensor_map_2d(&maps.b[i], bf16, 2, g[i].b, g[i].K,
+                                           kGated ? 2 * static_cast<uint64_t>(g[i].N) : g[i].N, kBK,
+                                           kGated ? kOutN : TL::kBRows));
+    ok = ok && encode_tensor_map_2d(&maps.y[i], bf16, 2, g[i].out, g[i].N, g[i].M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  if (n == 1) {
+    maps.a[1] = maps.a[0];
+    maps.b[1] = maps.b[0];
+    maps.y[1] = maps.y[0];
+  }
+  p.tiles = static_cast<int>(tiles);
+  p.act = g->act;
+  p.save = g->save0 != nullptr;
+  p.stall = stall_gate_up_loads();
+  p.bias = static_cast<const __nv_bfloat16*>(g->bias);
+  p.residual = static_cast<const __nv_bfloat16*>(g->residual);
+  p.timeout_ns = wait_limit_ns();
+  maps.save[0] = maps.save[1] = maps.y[0];
   if (p.save) {
-    const uint64_t ld = kGated ? 2 * static_cast<uint64_t>(g.N) : g.N;
-    if (!encode_tensor_map_2d_ld(&tmS0, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.save0, g.N, g.M, ld, 16, 32,
-                                 CU_TENSOR_MAP_SWIZZLE_64B))
-      return cudaErrorInvalidValue;
-    if (kGated && !encode_tensor_map_2d_ld(&tmS1, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.save0 + g.N, g.N, g.M, ld, 16,
-                                           32, CU_TENSOR_MAP_SWIZZLE_64B))
-      return cudaErrorInvalidValue;
+    const uint64_t ld = kGated ? 2 * static_cast<uint64_t>(g->N) : g->N;
+    for (int i = 0; i < (kGated ? 2 : 1); ++i)
+      if (!encode_tensor_map_2d_ld(&maps.save[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                                   g->save0 + static_cast<size_t>(i) * g->N, g->N, g->M, ld, 16, 32,
+                                   CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
   }
 
-  auto kernel = dense_gemm_kernel<kPair, kBN, kAmn, kBmn, kGated>;
+  auto kernel = dense_gemm_kernel<kPair, kBN, kMode>;
   static unsigned long long done = 0;
   cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
   if (err != cudaSuccess) return err;
-  int workers = std::min(num_sms / TL::kCtas, p.m_tiles * p.n_tiles);
+  int workers = std::min(num_sms / TL::kCtas, p.tiles);
   if (kPair) {
     // every pair of the persistent grid must be resident at once
     const int maxc = max_active_clusters(reinterpret_cast<const void*>(kernel), 2, kThreads, TL::kSmem);
@@ -482,38 +531,46 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmY, tmS0, tmS1, p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
-// Tile choice: the shape with the least estimated time, waves x (K steps x a
-// step + a tile's overhead). Measured on B200 with all SMs at work, a K step of 64
-// takes 0.34-0.38 us for 256 x 256 on a pair and 0.40-0.45 for 128 x 256 (a third
-// more bytes through shared memory), but still 0.28-0.31 at 128 columns: there the
-// issuing thread's own path (wait, four MMAs, commit) is as long as the MMAs of
-// 256 columns. So the narrow tiles only pay where they save a wave.
-template <bool kAmn, bool kBmn, bool kGated>
-cudaError_t launch_order(const DenseGemm& g, int num_sms, cudaStream_t st) {
-  const long long kb = (g.K + kBK - 1) / kBK;
-  auto cost = [&](int rows, int cols, int slots, int per_step) {
-    const int outn = kGated ? cols / 2 : cols;
-    const long long tiles = ((g.M + rows - 1ll) / rows) * ((g.N + outn - 1ll) / outn);
-    return ((tiles + slots - 1) / slots) * (kb * per_step + 1500);
+// Tile choice: the shape with the least estimated time (K steps x a step + a
+// tile's overhead, for the worker with the most tiles). Measured on B200 with
+// all SMs at work, a K step of 64 takes 0.34-0.38 us for 256 x 256 on a pair and
+// 0.40-0.45 for 128 x 256 (a third more bytes through shared memory), but still
+// 0.28-0.31 at 128 columns: there the issuing thread's own path (wait, four
+// MMAs, commit) is as long as the MMAs of 256 columns. So the narrow tiles only
+// pay where they save a wave.
+template <int kMode>
+cudaError_t launch_mode(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
+  auto cost = [&](int rows, int cols, int workers, int per_step) {
+    const int outn = kMode == kModeGated ? cols / 2 : cols;
+    long long tiles[2] = {0, 0}, each[2] = {0, 0};
+    for (int i = 0; i < n; ++i) {
+      tiles[i] = ((g[i].M + rows - 1ll) / rows) * ((g[i].N + outn - 1ll) / outn);
+      each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1500;
+    }
+    // worker w has the tiles w, w + workers, ... of the list: the most loaded is
+    // worker 0, or the one at which the first product's last round ends
+    const long long all = (tiles[0] + tiles[1] + workers - 1) / workers;
+    const long long full = std::min(all, (tiles[0] + workers - 1) / workers);
+    return full * each[0] + (all - full) * each[1];
   };
   const long long c[4] = {cost(256, 256, num_sms / 2, 347), cost(256, 128, num_sms / 2, 300),
                           cost(128, 256, num_sms, 410), cost(128, 128, num_sms, 290)};
   int best = 0;
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[best]) best = i;
-  if (g.force >= 0) best = g.force;
+  if (g->force >= 0) best = g->force;
   switch (best) {
     case 0:
-      return launch_t<true, 256, kAmn, kBmn, kGated>(g, num_sms, st);
+      return launch_t<true, 256, kMode>(g, n, num_sms, st);
     case 1:
-      return launch_t<true, 128, kAmn, kBmn, kGated>(g, num_sms, st);
+      return launch_t<true, 128, kMode>(g, n, num_sms, st);
     case 2:
-      return launch_t<false, 256, kAmn, kBmn, kGated>(g, num_sms, st);
+      return launch_t<false, 256, kMode>(g, n, num_sms, st);
     default:
-      return launch_t<false, 128, kAmn, kBmn, kGated>(g, num_sms, st);
+      return launch_t<false, 128, kMode>(g, n, num_sms, st);
   }
 }
 
@@ -522,14 +579,17 @@ cudaError_t launch_order(const DenseGemm& g, int num_sms, cudaStream_t st) {
 cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st) {
   switch (g.order) {
     case kGatedNT:
-      return launch_order<false, false, true>(g, num_sms, st);
+      return launch_mode<kModeGated>(&g, 1, num_sms, st);
     case kLinearNT:
-      return launch_order<false, false, false>(g, num_sms, st);
-    case kLinearNN:
-      return launch_order<false, true, false>(g, num_sms, st);
+      return launch_mode<kModeLinear>(&g, 1, num_sms, st);
     default:
-      return launch_order<true, true, false>(g, num_sms, st);
+      return launch_mode<kModeBackward>(&g, 1, num_sms, st);
   }
+}
+
+cudaError_t launch_dense_gemm_backward(const DenseGemm& dx, const DenseGemm& dw, int num_sms, cudaStream_t st) {
+  const DenseGemm g[2] = {dx.K >= dw.K ? dx : dw, dx.K >= dw.K ? dw : dx};  // the longer tiles first
+  return launch_mode<kModeBackward>(g, 2, num_sms, st);
 }
 
 }  // namespace moe

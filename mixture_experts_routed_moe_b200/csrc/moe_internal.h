@@ -131,6 +131,8 @@ struct DenseGemm {
 };
 
 cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st);
+// A kLinearNN and a kLinearTN product in one launch (neither may read the other's output).
+cudaError_t launch_dense_gemm_backward(const DenseGemm& dx, const DenseGemm& dw, int num_sms, cudaStream_t st);
 // The form for few tokens (M), weights streamed with K split over clusters.
 bool dense_small_supported(const DenseGemm& g);
 cudaError_t launch_dense_small(const DenseGemm& g, int num_sms, cudaStream_t st);
