@@ -50,11 +50,12 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 moe_status done(cudaError_t err) { return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 cudaError_t run(const DenseGemm& g, int sms, cudaStream_t st) {
-  return dense_small_supported(g) ? launch_dense_small(g, sms, st) : launch_dense_gemm(g, sms, st);
+  return dense_small_us(g, sms) < dense_gemm_us(g, sms) ? launch_dense_small(g, sms, st)
+                                                        : launch_dense_gemm(g, sms, st);
 }
 
-// dx = d W (d [T, M], W [M, K]) and dw = d^T x; either may be null. Few tokens'
-// dx streams the weights; else both products share one launch.
+// dx = d W (d [T, M], W [M, K]) and dw = d^T x; either may be null. Both
+// products share one launch, unless few tokens make dx faster as a stream of the weights.
 cudaError_t backward_products(const void* d, const void* x, const void* w, int T, int M, int K, void* dx, void* dw,
                               int sms, cudaStream_t st) {
   DenseGemm gx{}, gw{};
@@ -72,7 +73,9 @@ cudaError_t backward_products(const void* d, const void* x, const void* w, int T
   gw.a = d;
   gw.b = x;
   gw.out = dw;
-  if (dx != nullptr && dw != nullptr && !dense_small_supported(gx)) return launch_dense_gemm_backward(gx, gw, sms, st);
+  if (dx != nullptr && dw != nullptr &&
+      dense_small_us(gx, sms) + dense_gemm_us(gw, sms) >= dense_gemm_backward_us(gx, gw, sms))
+    return launch_dense_gemm_backward(gx, gw, sms, st);
   if (dx != nullptr) {
     const cudaError_t err = run(gx, sms, st);
     if (err != cudaSuccess) return err;

@@ -540,15 +540,21 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
 // 0.40-0.45 for 128 x 256 (a third more bytes through shared memory), but still
 // 0.28-0.31 at 128 columns: there the issuing thread's own path (wait, four
 // MMAs, commit) is as long as the MMAs of 256 columns. So the narrow tiles only
-// pay where they save a wave.
-template <int kMode>
-cudaError_t launch_mode(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
-  auto cost = [&](int rows, int cols, int workers, int per_step) {
-    const int outn = kMode == kModeGated ? cols / 2 : cols;
-    long long tiles[2] = {0, 0}, each[2] = {0, 0};
+// pay where they save a wave. The sum has 2.6 us for the launch, the first loads
+// and the last tile's end, and a third of the weights' time from HBM.
+struct Shape {
+  int best;
+  double us;
+};
+Shape choose_shape(const DenseGemm* g, int n, int num_sms) {
+  const bool gated = g->order == kGatedNT;
+  auto cost = [&](int rows, int cols, int workers, double per_step) {
+    const int outn = gated ? cols / 2 : cols;
+    long long tiles[2] = {0, 0};
+    double each[2] = {0, 0};
     for (int i = 0; i < n; ++i) {
       tiles[i] = ((g[i].M + rows - 1ll) / rows) * ((g[i].N + outn - 1ll) / outn);
-      each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1500;
+      each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1.5;
     }
     // worker w has the tiles w, w + workers, ... of the list: the most loaded is
     // worker 0, or the one at which the first product's last round ends
@@ -556,12 +562,19 @@ cudaError_t launch_mode(const DenseGemm* g, int n, int num_sms, cudaStream_t st)
     const long long full = std::min(all, (tiles[0] + workers - 1) / workers);
     return full * each[0] + (all - full) * each[1];
   };
-  const long long c[4] = {cost(256, 256, num_sms / 2, 347), cost(256, 128, num_sms / 2, 300),
-                          cost(128, 256, num_sms, 410), cost(128, 128, num_sms, 290)};
-  int best = 0;
+  const double c[4] = {cost(256, 256, num_sms / 2, 0.347), cost(256, 128, num_sms / 2, 0.300),
+                       cost(128, 256, num_sms, 0.410), cost(128, 128, num_sms, 0.290)};
+  Shape s{0, 0};
   for (int i = 1; i < 4; ++i)
-    if (c[i] < c[best]) best = i;
-  if (g->force >= 0) best = g->force;
+    if (c[i] < c[s.best]) s.best = i;
+  const double bytes = 2.0 * g->K * (static_cast<double>(g->N) * (gated ? 2 : 1) + (n == 2 ? g->M : 0));
+  s.us = 2.6 + c[s.best] + 0.35 * bytes / 6.0e6;
+  return s;
+}
+
+template <int kMode>
+cudaError_t launch_mode(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
+  const int best = choose_shape(g, n, num_sms).best;
   switch (best) {
     case 0:
       return launch_t<true, 256, kMode>(g, n, num_sms, st);
@@ -585,6 +598,12 @@ cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st) 
     default:
       return launch_mode<kModeBackward>(&g, 1, num_sms, st);
   }
+}
+
+double dense_gemm_us(const DenseGemm& g, int num_sms) { return choose_shape(&g, 1, num_sms).us; }
+double dense_gemm_backward_us(const DenseGemm& dx, const DenseGemm& dw, int num_sms) {
+  const DenseGemm g[2] = {dx.K >= dw.K ? dx : dw, dx.K >= dw.K ? dw : dx};
+  return choose_shape(g, 2, num_sms).us;
 }
 
 cudaError_t launch_dense_gemm_backward(const DenseGemm& dx, const DenseGemm& dw, int num_sms, cudaStream_t st) {

@@ -5,6 +5,7 @@
 //   linear:  out[t, n] = bf16(act(sum_k W[n,k] X[t,k] + bias[n]) + residual[t, n])
 //   gated:   out[t, n] = bf16(act(sum_k W[n,k] X[t,k]) * sum_k W[N+n,k] X[t,k])
 //
+// for batches of up to a few hundred tokens, in even token tiles of at most 128,
 // with W read K-major, or MN-major (linear only: dx = dz W of the backward
 // pass, where W^T's rows are the outputs). A unit is up to 128 weight rows
 // (gated: as many gate rows as up rows); a cluster of C CTAs owns a unit, CTA r
@@ -19,6 +20,7 @@
 // eight reduce. Every wait is bounded; a cluster with a wait that gave up
 // writes NaN.
 #include <algorithm>
+#include <limits>
 
 #include "dense_core.cuh"
 
@@ -30,12 +32,14 @@ constexpr int kThreads = 256;
 constexpr int kA = kTileM * kBK * 2;  // 16 KB of weights a stage
 constexpr int kLd = kTileM + 4;       // floats between two tokens' partial rows
 constexpr int kMaxStages = 12;
+constexpr int kTileTokens = 128;  // most tokens of a token tile
 
 struct SmallParams {
   int T, N, num_kb;
-  int n_pad;         // T rounded up to a multiple of 16 (MMA N)
+  int tile_t, tiles; // tokens of a token tile, token tiles
+  int n_pad;         // tile_t rounded up to a multiple of 16 (MMA N)
   uint32_t n_alloc;  // TMEM columns (power of two >= 32)
-  int stages, ring;  // TMA ring: stages of kA + n_pad * 128 bytes in `ring` bytes
+  int stages;        // of the ring, kA + n_pad * 128 bytes each
   int rows;          // outputs of a unit, a multiple of 8
   int act, stall;
   const __nv_bfloat16* bias;
@@ -46,9 +50,10 @@ struct SmallParams {
 };
 
 // Bytes of the ring: half an SM's shared memory (two CTAs of it, or one and the
-// next kernel's, which starts early), more only where the partial needs it.
-int ring_bytes(int T) { return T * kLd * 4 <= 98304 ? 98304 : 147456; }
-size_t small_smem(int ring) { return 1024 + static_cast<size_t>(ring) + (2 * kMaxStages + 1) * 8 + 32; }
+// next kernel's, which starts early). The partial of a token tile fits it.
+constexpr int kRing = 98304;
+static_assert(kTileTokens * kLd * 4 <= kRing, "the partial rows reuse the ring");
+size_t small_smem() { return 1024 + static_cast<size_t>(kRing) + (2 * kMaxStages + 1) * 8 + 32; }
 
 // The C partials at one place, added in rank order; all loads are in flight together.
 template <int kC>
@@ -68,15 +73,16 @@ __device__ __forceinline__ float4 sum_ranks(uint32_t addr) {
 
 // This CTA's share of the unit's outputs, four consecutive ones of a token per step.
 template <bool kGated, int kC>
-__device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int rank, bool aborted) {
+__device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
+                                       bool aborted) {
   const int per = p.rows / 4;
-  const int items = p.T * per;
+  const int items = nt * per;
   for (int i = rank * items / kC + threadIdx.x; i < (rank + 1) * items / kC; i += kThreads) {
     const int t = i / per, r = (i - t * per) * 4;
     const int n = n0 + r;
     if (n >= p.N) continue;  // N is a multiple of 8
     float v[4];
-    const size_t at = static_cast<size_t>(t) * p.N + n;
+    const size_t at = static_cast<size_t>(t0 + t) * p.N + n;
     const uint32_t sp = smem_u32(s_part + t * kLd + r);
     if (aborted) {
 #pragma unroll
@@ -84,7 +90,7 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
     } else if (kGated) {
       const float4 g = sum_ranks<kC>(sp), u = sum_ranks<kC>(sp + p.rows * 4);
       if (p.save != nullptr) {
-        float* s = p.save + 2 * static_cast<size_t>(t) * p.N + n;
+        float* s = p.save + 2 * static_cast<size_t>(t0 + t) * p.N + n;
         *reinterpret_cast<float4*>(s) = g;
         *reinterpret_cast<float4*>(s + p.N) = u;
       }
@@ -135,19 +141,22 @@ __global__ void __launch_bounds__(kThreads)
   const int kStages = p.stages;
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.ring);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_status = reinterpret_cast<int*>(s_tmem + 2);
-  float* s_part = reinterpret_cast<float*>(smem);  // [T][kLd], after the last MMA
+  float* s_part = reinterpret_cast<float*>(smem);  // [nt][kLd], after the last MMA
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int csize = static_cast<int>(cluster_nctarank());
   const int rank = static_cast<int>(cluster_ctarank());
-  const int unit = blockIdx.x / csize;
+  // consecutive clusters take the token tiles of one unit: its weights meet in L2
+  const int unit = blockIdx.x / csize / p.tiles;
   const int n0 = unit * p.rows;
+  const int t0 = (blockIdx.x / csize - unit * p.tiles) * p.tile_t;
+  const int nt = min(p.tile_t, p.T - t0);
   const int kb0 = rank * p.num_kb / csize, kb1 = (rank + 1) * p.num_kb / csize;
   // bytes a stage receives (an MN-major unit always has 128 rows)
   const uint32_t stage_bytes = static_cast<uint32_t>((kGated ? 2 : 1) * (kAmn ? 128 : p.rows) * 128 + kB);
@@ -195,7 +204,7 @@ __global__ void __launch_bounds__(kThreads)
         } else {
           tma_load_2d(a, &tmW, &full[stage], k0, n0);
         }
-        tma_load_2d(sB + stage * kB, &tmX, &full[stage], k0, 0);
+        tma_load_2d(sB + stage * kB, &tmX, &full[stage], k0, t0);
         if (++stage == kStages) {
           stage = 0;
           ph ^= 1;
@@ -248,7 +257,7 @@ __global__ void __launch_bounds__(kThreads)
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (c + i < p.T) s_part[(c + i) * kLd + r] = __uint_as_float(v[i]);
+          if (c + i < nt) s_part[(c + i) * kLd + r] = __uint_as_float(v[i]);
       }
     }
   }
@@ -261,16 +270,16 @@ __global__ void __launch_bounds__(kThreads)
     aborted |= ld_cluster_s32(cluster_map(smem_u32(const_cast<int*>(s_abort)), static_cast<uint32_t>(q))) != 0;
   switch (csize) {
     case 1:
-      finish<kGated, 1>(p, s_part, n0, rank, aborted);
+      finish<kGated, 1>(p, s_part, n0, t0, nt, rank, aborted);
       break;
     case 2:
-      finish<kGated, 2>(p, s_part, n0, rank, aborted);
+      finish<kGated, 2>(p, s_part, n0, t0, nt, rank, aborted);
       break;
     case 4:
-      finish<kGated, 4>(p, s_part, n0, rank, aborted);
+      finish<kGated, 4>(p, s_part, n0, t0, nt, rank, aborted);
       break;
     default:
-      finish<kGated, 8>(p, s_part, n0, rank, aborted);
+      finish<kGated, 8>(p, s_part, n0, t0, nt, rank, aborted);
   }
   // no CTA leaves while another may still read its shared memory
   cluster_sync();
@@ -280,6 +289,45 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Token tiles, rows of a unit and CTAs of a cluster.
+struct Plan {
+  int tile_t, tiles, rows, csize, ctas;
+  double us;  // estimated time; infinite where the CTAs would not be resident together
+};
+
+// The estimate, in us, from sweeps on B200 (weights of 2048 x 1408 to 14336 x
+// 4096, 16 to 1024 tokens): 5.5 for the launch, the first loads and the end; a
+// K step of a CTA at no less than 0.28, two CTAs of an SM sharing 150 KB/us;
+// the reduction with the partials it adds; 0.6 of the weights' time from HBM,
+// which the ring does not hide for so few steps. It is compared with the
+// tile kernel's, so it only has to be right to about a tenth.
+Plan plan_small(const DenseGemm& g, int num_sms) {
+  const int num_kb = (g.K + kBK - 1) / kBK;
+  const bool gated = g.order == kGatedNT;
+  const double weights = 2.0 * g.N * g.K * (gated ? 2 : 1) / 6.0e6;
+  Plan best{};
+  best.us = std::numeric_limits<double>::infinity();
+  for (int cap = 32; cap <= kTileTokens; cap += 32) {
+    const long long tiles = (g.M + cap - 1ll) / cap;
+    const int tile_t = static_cast<int>((g.M + tiles - 1) / tiles);
+    const int n_pad = (tile_t + 15) / 16 * 16;
+    for (int c = 1; c <= 8; c *= 2) {
+      if (c > 1 && 2 * c > num_kb) break;
+      for (int rows = gated ? 64 : 128; rows >= 64; rows -= 64) {
+        if (g.order == kLinearNN && rows != 128) continue;  // an MN-major unit is one box pair
+        const long long ctas = ((g.N + rows - 1ll) / rows) * tiles * c;
+        // clusters that fit at two CTAs an SM
+        if (ctas > num_sms * (c == 8 ? 1.78 : c == 4 ? 1.91 : 2.0)) continue;
+        const double share = ctas > num_sms ? 2 : 1;
+        const double step = std::max(0.28, share * ((gated ? 2 : 1) * rows * 128 + n_pad * 128) / 150e3);
+        const double us = 5.5 + (num_kb + c - 1) / c * step + 0.3 * c * n_pad / 64 + (c == 8 ? 0.4 : 0.0) + 0.6 * weights;
+        if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), us};
+      }
+    }
+  }
+  return best;
+}
+
 template <bool kAmn, bool kGated>
 cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   // here the weights are g.b (rows = outputs) and the tokens g.a
@@ -287,11 +335,15 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.T = g.M;
   p.N = g.N;
   p.num_kb = (g.K + kBK - 1) / kBK;
-  p.n_pad = (g.M + 15) / 16 * 16;
+  const Plan plan = plan_small(g, num_sms);
+  p.tile_t = plan.tile_t;
+  p.tiles = plan.tiles;
+  p.rows = plan.rows;
+  const int csize = plan.csize;
+  p.n_pad = (p.tile_t + 15) / 16 * 16;
   p.n_alloc = 32;
   while (p.n_alloc < static_cast<uint32_t>(p.n_pad)) p.n_alloc <<= 1;
-  p.ring = ring_bytes(g.M);
-  p.stages = std::min(kMaxStages, p.ring / (kA + p.n_pad * kBK * 2));
+  p.stages = std::min(kMaxStages, kRing / (kA + p.n_pad * kBK * 2));
   p.act = g.act;
   p.stall = stall_gate_up_loads();
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
@@ -299,23 +351,6 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.out = static_cast<__nv_bfloat16*>(g.out);
   p.save = g.save0;
   p.timeout_ns = wait_limit_ns();
-  // the partial rows reuse the ring
-  if (p.n_pad > 256 || g.M * kLd * 4 > p.ring) return cudaErrorInvalidValue;
-
-  // The widest cluster whose CTAs all fit two to an SM and have K steps to
-  // share. Many tokens make the reduction of eight partials dearer than it
-  // saves; linear units are halved there while the CTAs do not fill the SMs.
-  const int cmax = g.M <= 32 ? 8 : 4;
-  p.rows = kGated ? 64 : 128;
-  auto units_of = [&](int rows) { return (g.N + rows - 1) / rows; };
-  int csize = cmax;
-  while (csize > 1 && (static_cast<long long>(units_of(p.rows)) * csize > 2ll * num_sms || csize * 2 > p.num_kb))
-    csize >>= 1;
-  if (!kGated && !kAmn && csize == 4 && units_of(128) * csize < num_sms * 4 / 5) p.rows = 64;
-  if (g.force >= 0) {  // csize in the low byte, rows above
-    csize = g.force & 255;
-    p.rows = g.force >> 8;
-  }
 
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap tmW, tmX;
@@ -330,11 +365,10 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   static unsigned long long done = 0;
   cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
   if (err != cudaSuccess) return err;
-  const int units = (g.N + p.rows - 1) / p.rows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units * csize));
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = small_smem(p.ring);
+  cfg.dynamicSmemBytes = small_smem();
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -350,8 +384,8 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-bool dense_small_supported(const DenseGemm& g) {
-  return g.order != kLinearTN && g.M <= kDenseSmallT;
+double dense_small_us(const DenseGemm& g, int num_sms) {
+  return g.order == kLinearTN ? std::numeric_limits<double>::infinity() : plan_small(g, num_sms).us;
 }
 
 cudaError_t launch_dense_small(const DenseGemm& g, int num_sms, cudaStream_t st) {

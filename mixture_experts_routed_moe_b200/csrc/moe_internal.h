@@ -107,7 +107,6 @@ cudaError_t launch_fused_decode(const moe_shape* s, const Plan& p, const void* x
 
 constexpr int kActNone = MOE_ACT_NONE;
 constexpr int kNormBackwardBlocks = 296;  // row classes of the norm's weight gradient (two per SM of a B200)
-constexpr int kDenseSmallT = 64;          // tokens up to which the weight-streaming kernel runs
 
 // Operand orders of a dense GEMM with out [M, N].
 enum DenseOrder {
@@ -127,15 +126,19 @@ struct DenseGemm {
   const void* bias = nullptr;      // [N] bf16
   const void* residual = nullptr;  // [M, N] bf16, may be out
   float* save0 = nullptr;          // fp32 pre-activations: linear [M, N], gated [M, 2N]
-  int force = -1;                  // tile shape (a measurement's choice), -1 the rule's
 };
 
 cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st);
 // A kLinearNN and a kLinearTN product in one launch (neither may read the other's output).
 cudaError_t launch_dense_gemm_backward(const DenseGemm& dx, const DenseGemm& dw, int num_sms, cudaStream_t st);
 // The form for few tokens (M), weights streamed with K split over clusters.
-bool dense_small_supported(const DenseGemm& g);
 cudaError_t launch_dense_small(const DenseGemm& g, int num_sms, cudaStream_t st);
+
+// Estimated times in us, by which the entry points choose between the forms
+// (infinite where a form does not apply).
+double dense_gemm_us(const DenseGemm& g, int num_sms);
+double dense_gemm_backward_us(const DenseGemm& dx, const DenseGemm& dw, int num_sms);
+double dense_small_us(const DenseGemm& g, int num_sms);
 
 cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T, int I, int act, int num_sms,
                               cudaStream_t st);
