@@ -210,8 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int worker = blockIdx.x / TL::kCtas, nworkers = gridDim.x / TL::kCtas;
 
   if (warp == 0) {
-    if (lane == 0 && !p.stall) {
+    if (!p.stall) {
       // ---------------- TMA producer ----------------
+      const bool one = elect_one();
       int stage = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -224,47 +225,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int up_row = p.prod[0].N;  // gated: the first up row of B
         const int m0 = (c.m * TL::kCtas + rank) * kTileM;
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait_bounded(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) {
+          if (!warp_wait(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) {
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(&full[stage], TL::kCtas * TL::kStage);
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
-            if (kPair)
-              tma_load_2d_pair(dst, map, leader_addr(&full[stage]), x, y);
-            else
-              tma_load_2d(dst, map, &full[stage], x, y);
-          };
-          uint8_t* a = sA + stage * TL::kA;
-          uint8_t* b = sB + stage * TL::kB;
-          const int k0 = kb * kBK;
-          if (a_mn) {
-            load(a, tmA, m0, k0);
-            load(a + 8192, tmA, m0 + 64, k0);
-          } else {
-            load(a, tmA, k0, m0);
-          }
-          if (kGated) {
-            if (kPair) {
-              load(b, tmB, k0, c.n * kOutN + rank * up_row);
+          if (one) {
+            if (leader) mbar_arrive_expect_tx(&full[stage], TL::kCtas * TL::kStage);
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+              if (kPair)
+                tma_load_2d_pair(dst, map, leader_addr(&full[stage]), x, y);
+              else
+                tma_load_2d(dst, map, &full[stage], x, y);
+            };
+            uint8_t* a = sA + stage * TL::kA;
+            uint8_t* b = sB + stage * TL::kB;
+            const int k0 = kb * kBK;
+            if (a_mn) {
+              load(a, tmA, m0, k0);
+              load(a + 8192, tmA, m0 + 64, k0);
             } else {
-              load(b, tmB, k0, c.n * kOutN);
-              load(b + TL::kB / 2, tmB, k0, c.n * kOutN + up_row);
+              load(a, tmA, k0, m0);
             }
-          } else if (kBmn) {
+            if (kGated) {
+              if (kPair) {
+                load(b, tmB, k0, c.n * kOutN + rank * up_row);
+              } else {
+                load(b, tmB, k0, c.n * kOutN);
+                load(b + TL::kB / 2, tmB, k0, c.n * kOutN + up_row);
+              }
+            } else if (kBmn) {
 #pragma unroll
-            for (int j = 0; j < TL::kBRows / 64; ++j)
-              load(b + j * 8192, tmB, c.n * kBN + rank * TL::kBRows + 64 * j, k0);
-          } else {
-            load(b, tmB, k0, c.n * kBN + rank * TL::kBRows);
+              for (int j = 0; j < TL::kBRows / 64; ++j)
+                load(b + j * 8192, tmB, c.n * kBN + rank * TL::kBRows + 64 * j, k0);
+            } else {
+              load(b, tmB, k0, c.n * kBN + rank * TL::kBRows);
+            }
           }
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             ph ^= 1;
           }
         }
       }
-      if (!ok && leader) {
+      if (!ok && leader && one) {
         // let the copies already issued (of both CTAs) land before the CTA can exit
         for (int i = 0; i < kStages; ++i) {
           if (--stage < 0) {
@@ -277,13 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ---------------- MMA issuer ----------------
+      const bool one = elect_one();
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       for (int tile = worker; ok && tile < total; tile += nworkers) {
-        if (!mbar_wait_bounded(&tempty[acc], aph ^ 1, s_abort, s_status, p.timeout_ns)) break;
+        if (!warp_wait(&tempty[acc], aph ^ 1, s_abort, s_status, p.timeout_ns)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
         const int prob = kMode == kModeBackward && tile >= p.first_tiles ? 1 : 0;
@@ -292,45 +297,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = a_mn ? idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, true, kBmn)
                                     : idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, false, kBmn);
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait_bounded(&full[stage], ph, s_abort, s_status, p.timeout_ns)) {
+          if (!warp_wait(&full[stage], ph, s_abort, s_status, p.timeout_ns)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + stage * TL::kA);
-          const uint32_t b0 = smem_u32(sB + stage * TL::kB);
+          if (one) {
+            const uint32_t a0 = smem_u32(sA + stage * TL::kA);
+            const uint32_t b0 = smem_u32(sB + stage * TL::kB);
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t da = a_mn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32);
-            const uint64_t db = kBmn ? sdesc_mnmajor_sw128(b0 + k * 2048) : sdesc_kmajor_sw128(b0 + k * 32);
+            for (int k = 0; k < kBK / 16; ++k) {
+              const uint64_t da = a_mn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32);
+              const uint64_t db = kBmn ? sdesc_mnmajor_sw128(b0 + k * 2048) : sdesc_kmajor_sw128(b0 + k * 32);
+              if (kPair)
+                umma_bf16_pair(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+              else
+                umma_bf16(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+            }
             if (kPair)
-              umma_bf16_pair(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+              umma_commit_pair_mc(&empty[stage], 0x3);
             else
-              umma_bf16(d, da, db, idesc, (kb | k) != 0 ? 1u : 0u);
+              umma_commit(&empty[stage]);
+            if (kb == num_kb - 1) {
+              if (kPair)
+                umma_commit_pair_mc(&tfull[acc], 0x3);
+              else
+                umma_commit(&tfull[acc]);
+            }
           }
-          if (kPair)
-            umma_commit_pair_mc(&empty[stage], 0x3);
-          else
-            umma_commit(&empty[stage]);
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             ph ^= 1;
           }
         }
         if (!ok) break;
-        if (kPair)
-          umma_commit_pair_mc(&tfull[acc], 0x3);
-        else
-          umma_commit(&tfull[acc]);
         acc ^= 1;
         if (acc == 0) aph ^= 1;
       }
-      if (kPair)
-        umma_commit_pair(drain);
-      else
-        umma_commit(drain);
-      int never = 0;
-      mbar_wait_bounded(drain, 0, &never, s_status, p.timeout_ns);
+      if (one) {
+        if (kPair)
+          umma_commit_pair(drain);
+        else
+          umma_commit(drain);
+        int never = 0;
+        mbar_wait_bounded(drain, 0, &never, s_status, p.timeout_ns);
+      }
     }
   } else {
     // ---------------- epilogue (own 128 rows) ----------------

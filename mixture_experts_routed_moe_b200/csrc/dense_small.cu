@@ -186,31 +186,35 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0 && !p.stall) {
+    if (!p.stall) {
+      const bool one = elect_one();
       int stage = 0;
       uint32_t ph = 0;
       int kb = kb0;
       for (; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) break;
-        mbar_arrive_expect_tx(&full[stage], stage_bytes);
-        uint8_t* a = sA + stage * kA;
-        const int k0 = kb * kBK;
-        if (kAmn) {
-          tma_load_2d(a, &tmW, &full[stage], n0, k0);
-          tma_load_2d(a + 8192, &tmW, &full[stage], n0 + 64, k0);
-        } else if (kGated) {
-          tma_load_2d(a, &tmW, &full[stage], k0, n0);
-          tma_load_2d(a + p.rows * 128, &tmW, &full[stage], k0, p.N + n0);
-        } else {
-          tma_load_2d(a, &tmW, &full[stage], k0, n0);
+        if (!warp_wait(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) break;
+        if (one) {
+          mbar_arrive_expect_tx(&full[stage], stage_bytes);
+          uint8_t* a = sA + stage * kA;
+          const int k0 = kb * kBK;
+          if (kAmn) {
+            tma_load_2d(a, &tmW, &full[stage], n0, k0);
+            tma_load_2d(a + 8192, &tmW, &full[stage], n0 + 64, k0);
+          } else if (kGated) {
+            tma_load_2d(a, &tmW, &full[stage], k0, n0);
+            tma_load_2d(a + p.rows * 128, &tmW, &full[stage], k0, p.N + n0);
+          } else {
+            tma_load_2d(a, &tmW, &full[stage], k0, n0);
+          }
+          tma_load_2d(sB + stage * kB, &tmX, &full[stage], k0, t0);
         }
-        tma_load_2d(sB + stage * kB, &tmX, &full[stage], k0, t0);
+        __syncwarp();
         if (++stage == kStages) {
           stage = 0;
           ph ^= 1;
         }
       }
-      if (kb < kb1) {
+      if (kb < kb1 && one) {
         // let the copies already issued land before the shared memory is reused
         for (int i = 0; i < kStages; ++i) {
           if (--stage < 0) {
@@ -223,13 +227,14 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32_major(kTileM, p.n_pad, kAmn, false);
-      int stage = 0;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&full[stage], ph, s_abort, s_status, p.timeout_ns)) break;
-        tc_fence_after();
+    const bool one = elect_one();
+    const uint32_t idesc = idesc_bf16_f32_major(kTileM, p.n_pad, kAmn, false);
+    int stage = 0;
+    uint32_t ph = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_wait(&full[stage], ph, s_abort, s_status, p.timeout_ns)) break;
+      tc_fence_after();
+      if (one) {
         const uint32_t a0 = smem_u32(sA + stage * kA);
         const uint32_t b0 = smem_u32(sB + stage * kB);
 #pragma unroll
@@ -237,13 +242,14 @@ __global__ void __launch_bounds__(kThreads)
           umma_bf16(tmem_base, kAmn ? sdesc_mnmajor_sw128(a0 + k * 2048) : sdesc_kmajor_sw128(a0 + k * 32),
                     sdesc_kmajor_sw128(b0 + k * 32), idesc, (kb > kb0 || k != 0) ? 1u : 0u);
         umma_commit(&empty[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          ph ^= 1;
-        }
       }
-      umma_commit(tfull);
+      __syncwarp();
+      if (++stage == kStages) {
+        stage = 0;
+        ph ^= 1;
+      }
     }
+    if (one) umma_commit(tfull);
   } else if (warp < 6) {
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
