@@ -52,7 +52,7 @@ struct Product {
 
 struct GemmParams {
   Product prod[2];  // the second only in backward mode
-  int first_tiles, tiles;  // tiles of the first product, of both
+  int first_tiles, full, tiles;  // tiles of the first product; whole tiles of both, list length with the half ones
   int act, save, stall;
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
@@ -76,11 +76,16 @@ struct Tile {
 };
 
 struct Coord {
-  int prob, m, n;
+  int prob, m, x, nb;  // product, row block, first output column, MMA N of the tile
 };
-template <int kMode>
-__device__ __forceinline__ Coord tile_coord(const GemmParams& p, int tile) {
+// Entry `i` of the list: the first `full` are whole tiles, then the two halves
+// (kBN / 2 columns) of each of the rest.
+template <int kMode, int kBN>
+__device__ __forceinline__ Coord tile_coord(const GemmParams& p, int i) {
+  constexpr int kOutN = kMode == kModeGated ? kBN / 2 : kBN;
   Coord c;
+  const bool half = i >= p.full;
+  int tile = half ? p.full + (i - p.full) / 2 : i;
   c.prob = kMode == kModeBackward && tile >= p.first_tiles ? 1 : 0;
   if (c.prob) tile -= p.first_tiles;
   const int m_tiles = p.prod[c.prob].m_tiles;
@@ -88,8 +93,10 @@ __device__ __forceinline__ Coord tile_coord(const GemmParams& p, int tile) {
   const int g = tile / per;
   const int gm = min(kGroupM, m_tiles - g * kGroupM);
   const int r = tile - g * per;
-  c.n = r / gm;
-  c.m = g * kGroupM + (r - c.n * gm);
+  const int n = r / gm;
+  c.m = g * kGroupM + (r - n * gm);
+  c.nb = half ? kBN / 2 : kBN;
+  c.x = n * kOutN + (half ? ((i - p.full) & 1) * (kOutN / 2) : 0);
   return c;
 }
 
@@ -153,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kGated = kMode == kModeGated;
   constexpr bool kBmn = kMode == kModeBackward;
   constexpr int kStages = TL::kStages;
-  constexpr int kOutN = kGated ? kBN / 2 : kBN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sA = smem;
@@ -217,20 +223,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = worker; ok && tile < total; tile += nworkers) {
-        const Coord c = tile_coord<kMode>(p, tile);
+        const Coord c = tile_coord<kMode, kBN>(p, tile);
         const int num_kb = p.prod[c.prob].num_kb;
         const bool a_mn = kMode == kModeBackward && p.prod[c.prob].a_mn;
         const CUtensorMap* tmA = &maps.a[c.prob];
         const CUtensorMap* tmB = &maps.b[c.prob];
         const int up_row = p.prod[0].N;  // gated: the first up row of B
         const int m0 = (c.m * TL::kCtas + rank) * kTileM;
+        const int rows64 = c.nb / TL::kCtas / 64;  // boxes of B in this CTA
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) {
             ok = false;
             break;
           }
           if (one) {
-            if (leader) mbar_arrive_expect_tx(&full[stage], TL::kCtas * TL::kStage);
+            if (leader) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(TL::kCtas * TL::kA + c.nb * kBK * 2));
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
               if (kPair)
                 tma_load_2d_pair(dst, map, leader_addr(&full[stage]), x, y);
@@ -246,19 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               load(a, tmA, k0, m0);
             }
-            if (kGated) {
-              if (kPair) {
-                load(b, tmB, k0, c.n * kOutN + rank * up_row);
-              } else {
-                load(b, tmB, k0, c.n * kOutN);
-                load(b + TL::kB / 2, tmB, k0, c.n * kOutN + up_row);
-              }
-            } else if (kBmn) {
+            // B in boxes of 64 of its rows (columns of the output)
 #pragma unroll
-              for (int j = 0; j < TL::kBRows / 64; ++j)
-                load(b + j * 8192, tmB, c.n * kBN + rank * TL::kBRows + 64 * j, k0);
-            } else {
-              load(b, tmB, k0, c.n * kBN + rank * TL::kBRows);
+            for (int j = 0; j < TL::kBRows / 64; ++j) {
+              if (j >= rows64) break;
+              if (kGated) {
+                const int row = kPair ? c.x + rank * up_row + 64 * j
+                                      : (j < rows64 / 2 ? c.x + 64 * j : c.x + up_row + 64 * (j - rows64 / 2));
+                load(b + j * 8192, tmB, k0, row);
+              } else if (kBmn) {
+                load(b + j * 8192, tmB, c.x + rank * (c.nb / 2) + 64 * j, k0);
+              } else {
+                load(b + j * 8192, tmB, k0, c.x + rank * (c.nb / 2) + 64 * j);
+              }
             }
           }
           __syncwarp();
@@ -291,11 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(&tempty[acc], aph ^ 1, s_abort, s_status, p.timeout_ns)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
-        const int prob = kMode == kModeBackward && tile >= p.first_tiles ? 1 : 0;
-        const int num_kb = p.prod[prob].num_kb;
-        const bool a_mn = kMode == kModeBackward && p.prod[prob].a_mn;
-        const uint32_t idesc = a_mn ? idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, true, kBmn)
-                                    : idesc_bf16_f32_major(kTileM * TL::kCtas, kBN, false, kBmn);
+        const Coord c = tile_coord<kMode, kBN>(p, tile);
+        const int num_kb = p.prod[c.prob].num_kb;
+        const bool a_mn = kMode == kModeBackward && p.prod[c.prob].a_mn;
+        const uint32_t idesc = idesc_bf16_f32_major(kTileM * TL::kCtas, c.nb, a_mn, kBmn);
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!warp_wait(&full[stage], ph, s_abort, s_status, p.timeout_ns)) {
             ok = false;
@@ -347,17 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- epilogue (own 128 rows) ----------------
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    constexpr int kCols = kOutN / 2;  // output columns of this warp
     Stager st{sY + (warp - 2) * 2 * kBox, 0, lane};
     int acc = 0;
     uint32_t aph = 0;
     int tile = worker;
     for (; tile < total; tile += nworkers) {
-      const Coord co = tile_coord<kMode>(p, tile);
+      const Coord co = tile_coord<kMode, kBN>(p, tile);
+      const int outn = kGated ? co.nb / 2 : co.nb, cols = outn / 2;  // output columns of the tile, of this warp
       const int M = p.prod[co.prob].M, N = p.prod[co.prob].N;
       const CUtensorMap* tmY = &maps.y[co.prob];
       const int y0 = (co.m * TL::kCtas + rank) * kTileM + quad * 32;
-      const int x0 = co.n * kOutN + half * kCols;
+      const int x0 = co.x + half * cols;
       const bool rows = y0 < M;
       const bool mine = y0 + lane < M;
       // the residual of the first columns is on its way while the tile's MMAs run
@@ -375,15 +381,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
-                          static_cast<uint32_t>(acc * kBN + half * kCols);
+                          static_cast<uint32_t>(acc * kBN + half * cols);
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
+      for (int c = 0; c < cols; c += 32) {
         const int x = x0 + c;
         float v[32];
         if (kGated) {
           float u[32];
           tmem_load32(tb + c, v);
-          tmem_load32(tb + kOutN + c, u);
+          tmem_load32(tb + outn + c, u);
           if (p.save) {
             st.store_f32(&maps.save[0], v, x, y0, N, rows);
             st.store_f32(&maps.save[1], u, x, y0, N, rows);
@@ -426,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v[8 * i + 2 * q + 1] += bf16_hi(w[q]);
               }
             }
-            if (c + 32 < kCols) load_res(x + 32);
+            if (c + 32 < cols) load_res(x + 32);
           }
         }
         st.store_bf16(tmY, v, x, y0, rows && x < N);
@@ -444,12 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // a wait gave up (never in normal operation): mark what this warp did not compute
     for (; tile < total; tile += nworkers) {
-      const Coord co = tile_coord<kMode>(p, tile);
+      const Coord co = tile_coord<kMode, kBN>(p, tile);
+      const int cols = (kGated ? co.nb / 2 : co.nb) / 2;
       const Product& pr = p.prod[co.prob];
       const int y = (co.m * TL::kCtas + rank) * kTileM + quad * 32 + lane;
-      const int x0 = co.n * kOutN + half * kCols;
+      const int x0 = co.x + half * cols;
       if (y < pr.M)
-        for (int x = x0; x < min(x0 + kCols, pr.N); ++x)
+        for (int x = x0; x < min(x0 + cols, pr.N); ++x)
           pr.out[static_cast<size_t>(y) * pr.N + x] = __ushort_as_bfloat16(0x7FC0);
     }
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
@@ -464,6 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       tmem_dealloc(tmem_base, 2 * kBN);
   }
+}
+
+// The tiles of a last round that would leave half of the workers idle are
+// computed in halves of 128 columns, twice as many workers at two thirds of a
+// tile's time.
+bool halve_last(long long tiles, int workers) {
+  const long long rest = tiles % workers;
+  return rest > 0 && 2 * rest <= workers;
 }
 
 template <bool kPair, int kBN, int kMode>
@@ -492,8 +507,7 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
     ok = ok && (kMode == kModeBackward
                     ? encode_tensor_map_2d(&maps.b[i], bf16, 2, g[i].b, g[i].N, g[i].K, 64, kBK)
                     : encode_tensor_map_2d(&maps.b[i], bf16, 2, g[i].b, g[i].K,
-                                           kGated ? 2 * static_cast<uint64_t>(g[i].N) : g[i].N, kBK,
-                                           kGated ? kOutN : TL::kBRows));
+                                           kGated ? 2 * static_cast<uint64_t>(g[i].N) : g[i].N, kBK, 64));
     ok = ok && encode_tensor_map_2d(&maps.y[i], bf16, 2, g[i].out, g[i].N, g[i].M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return cudaErrorInvalidValue;
   }
@@ -502,7 +516,6 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
     maps.b[1] = maps.b[0];
     maps.y[1] = maps.y[0];
   }
-  p.tiles = static_cast<int>(tiles);
   p.act = g->act;
   p.save = g->save0 != nullptr;
   p.stall = stall_gate_up_loads();
@@ -523,12 +536,18 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
   static unsigned long long done = 0;
   cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
   if (err != cudaSuccess) return err;
-  int workers = std::min(num_sms / TL::kCtas, p.tiles);
+  int workers = num_sms / TL::kCtas;
   if (kPair) {
     // every pair of the persistent grid must be resident at once
     const int maxc = max_active_clusters(reinterpret_cast<const void*>(kernel), 2, kThreads, TL::kSmem);
     if (maxc > 0) workers = std::min(workers, maxc);
   }
+  p.full = p.tiles = static_cast<int>(tiles);
+  if (kBN == 256 && halve_last(tiles, workers)) {
+    p.full -= p.tiles % workers;
+    p.tiles += p.tiles % workers;
+  }
+  workers = std::min(workers, p.tiles);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::max(1, workers) * TL::kCtas));
   cfg.blockDim = dim3(kThreads);
@@ -550,9 +569,9 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
 // tile's overhead, for the worker with the most tiles). Measured on B200 with
 // all SMs at work, a K step of 64 takes 0.34-0.38 us for 256 x 256 on a pair and
 // 0.40-0.45 for 128 x 256 (a third more bytes through shared memory), but still
-// 0.28-0.31 at 128 columns: there the issuing thread's own path (wait, four
-// MMAs, commit) is as long as the MMAs of 256 columns. So the narrow tiles only
-// pay where they save a wave. The sum has 2.6 us for the launch, the first loads
+// 0.26-0.29 at 128 columns: there the issuing warp's own path (wait, four MMAs,
+// commit: 0.20) and the bytes through shared memory, the same for half the
+// products, pace it. So the narrow tiles only pay where they save a wave. The sum has 2.6 us for the launch, the first loads
 // and the last tile's end, and a third of the weights' time from HBM.
 struct Shape {
   int best;
@@ -572,10 +591,11 @@ Shape choose_shape(const DenseGemm* g, int n, int num_sms) {
     // worker 0, or the one at which the first product's last round ends
     const long long all = (tiles[0] + tiles[1] + workers - 1) / workers;
     const long long full = std::min(all, (tiles[0] + workers - 1) / workers);
-    return full * each[0] + (all - full) * each[1];
+    const double halved = cols == 256 && halve_last(tiles[0] + tiles[1], workers) ? 0.3 * each[n - 1] : 0.0;
+    return full * each[0] + (all - full) * each[1] - halved;
   };
-  const double c[4] = {cost(256, 256, num_sms / 2, 0.347), cost(256, 128, num_sms / 2, 0.300),
-                       cost(128, 256, num_sms, 0.410), cost(128, 128, num_sms, 0.290)};
+  const double c[4] = {cost(256, 256, num_sms / 2, 0.347), cost(256, 128, num_sms / 2, 0.270),
+                       cost(128, 256, num_sms, 0.410), cost(128, 128, num_sms, 0.260)};
   Shape s{0, 0};
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[s.best]) s.best = i;
