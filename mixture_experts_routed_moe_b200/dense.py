@@ -12,6 +12,7 @@ every call can be captured in a CUDA graph after one eager call.
 from __future__ import annotations
 
 import contextlib
+import functools
 import typing
 
 import torch
@@ -21,60 +22,67 @@ from . import _FLOAT8, ACT, _check, _need, lib
 _BF16 = torch.bfloat16
 _F32 = torch.float32
 _LINEAR_ACT = dict(ACT, none=-1)
-_NO_GUARD = contextlib.nullcontext()
 
 
-def _tensor(t, name, dtype, shape, device):
-    """One tensor of the given type and sizes, contiguous, on `device` (a CUDA
-    device). The common case is one line: small calls are bound by the host."""
-    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.is_contiguous()
-            and t.device == device):
+@contextlib.contextmanager
+def _on(device, stream):
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
+    else:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _operator(fn):
+    """An entry point whose first argument fixes the device: it runs with that
+    device current and the caller's stream, if given, as the current stream, so
+    that outputs and workspaces allocated inside belong to the stream that uses
+    them. The common case (current device, current stream) is passed straight on:
+    small calls are bound by the host."""
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            return fn(first, *args, **kw)  # refused inside, by name
+        if stream is None and first.get_device() == torch._C._cuda_getDevice():
+            return fn(first, *args, **kw)
+        with _on(first.device, stream):
+            return fn(first, *args, **kw)
+
+    return call
+
+
+def _current_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _tensor(t, name, dtype, shape, index):
+    """The address of a tensor of the given type and sizes, contiguous, on CUDA
+    device `index`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == index):
         return t.data_ptr()
     _need(t, name, (dtype,), len(shape), shape, cuda=False)
-    raise ValueError(f"{name} is on {t.device}, x on {device}: all tensors must share one CUDA device")
-
-
-def _optional(t, name, dtype, shape, device):
-    return None if t is None else _tensor(t, name, dtype, shape, device)
+    raise ValueError(f"{name} is on {t.device}, not cuda:{index}: all tensors must share one CUDA device")
 
 
 def _first(t, name):
-    """The tensor that fixes the token count and the device: (T, columns, device)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == _BF16 and t.dim() == 2 and t.is_contiguous() and t.is_cuda):
+    """The tensor that fixes the token count and the device: (shape, device index)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.dim() == 2 and t.is_contiguous() and t.is_cuda):
         _need(t, name, (_BF16,), 2, cuda=False)
         raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
-    T, n = t.shape
-    return T, n, t.device
+    return t.shape, t.get_device()
 
 
-def _launch(device, stream):
-    """(guard, raw stream) of a call on `device`. Under the guard the device is
-    the current one and the caller's stream, if given, the current stream, so
-    outputs and workspaces allocated there belong to the stream that uses them."""
-    index = device.index
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream), stream.cuda_stream
-    guard = _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
-    return guard, torch._C._cuda_getCurrentRawStream(index)
-
-
-def _output(t, name, like, shape, device):
-    """The caller's bf16 output tensor after its checks, or a new one (of
-    like's type and device: `like` is an input)."""
-    if t is None:
-        return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
-    _tensor(t, name, _BF16, shape, device)
-    return t
-
-
-def _workspace(ws, need, device):
+def _workspace(ws, need, like):
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return like.new_empty(need, dtype=torch.uint8)
     _need(ws, "workspace", (torch.uint8,), 1, cuda=False)
-    if ws.device != device:
-        raise ValueError(f"workspace is on {ws.device}, x on {device}: all tensors must share one CUDA device")
+    if ws.device != like.device:
+        raise ValueError(f"workspace is on {ws.device}, not {like.device}: all tensors must share one CUDA device")
     return ws
 
 
@@ -97,143 +105,146 @@ class RMSNormOutput(typing.NamedTuple):
     rstd: torch.Tensor | None = None
 
 
+@_operator
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False, rstd: bool = False, out=None,
-             residual_out=None, stream=None) -> RMSNormOutput:
+             residual_out=None) -> RMSNormOutput:
     """moe_rms_norm: s = x + residual (rounded to bf16, the residual stream),
     y = s * (mean(s^2) + eps)^(-1/2) * weight. ``out`` and ``residual_out`` may be
     x or residual for an in-place step. ``quantize`` adds y in the form of the
-    FP8 experts' activations (H a multiple of 128)."""
-    T, H, device = _first(x, "x")
-    w = _tensor(weight, "weight", _BF16, (H,), device)
-    r = _optional(residual, "residual", _BF16, (T, H), device)
-    guard, st = _launch(device, stream)
-    with guard:
-        y = _output(out, "out", x, (T, H), device)
-        s, sp = x, None
-        if residual is not None:
-            s = _output(residual_out, "residual_out", x, (T, H), device)
-            sp = s.data_ptr()
-        elif residual_out is not None:
-            raise ValueError("residual_out was given without a residual")
-        codes = scales = rs = None
-        if quantize:
-            codes = torch.empty((T, H), dtype=_FLOAT8, device=device)
-            scales = torch.empty((T, H // 128), dtype=_F32, device=device)
-        if rstd:
-            rs = torch.empty((T,), dtype=_F32, device=device)
-        _check(lib().moe_rms_norm(x.data_ptr(), r, w, T, H, eps, y.data_ptr(), sp,
-                                  None if codes is None else codes.data_ptr(),
-                                  None if scales is None else scales.data_ptr(),
-                                  None if rs is None else rs.data_ptr(), st), "moe_rms_norm")
+    FP8 experts' activations (H a multiple of 128). ``stream``: launch there."""
+    shape, dev = _first(x, "x")
+    T, H = shape
+    w = _tensor(weight, "weight", _BF16, (H,), dev)
+    r = sp = cp = kp = rp = codes = scales = rs = None
+    s = x
+    if residual is not None:
+        r = _tensor(residual, "residual", _BF16, shape, dev)
+        s = torch.empty_like(x) if residual_out is None else residual_out
+        sp = _tensor(s, "residual_out", _BF16, shape, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out was given without a residual")
+    y = torch.empty_like(x) if out is None else out
+    yp = _tensor(y, "out", _BF16, shape, dev)
+    if quantize:
+        codes = torch.empty_like(x, dtype=_FLOAT8)
+        scales = x.new_empty((T, H // 128), dtype=_F32)
+        cp, kp = codes.data_ptr(), scales.data_ptr()
+    if rstd:
+        rs = x.new_empty(T, dtype=_F32)
+        rp = rs.data_ptr()
+    _check(lib().moe_rms_norm(x.data_ptr(), r, w, T, H, eps, yp, sp, cp, kp, rp, _current_stream(dev)), "moe_rms_norm")
     return RMSNormOutput(y, s, codes, scales, rs)
 
 
-def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, workspace=None, stream=None):
+@_operator
+def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, workspace=None):
     """moe_rms_norm_backward: (dx bf16 [T,H], dw bf16 [H]) from the gradient dy at
     y and dresidual at the residual stream; s, weight and rstd are the
     forward's (``RMSNormOutput.residual`` and ``.rstd``). dx is the gradient of x
-    and of the residual alike."""
-    T, H, device = _first(dy, "dy")
-    sp = _tensor(s, "s", _BF16, (T, H), device)
-    w = _tensor(weight, "weight", _BF16, (H,), device)
-    r = _tensor(rstd, "rstd", _F32, (T,), device)
-    dr = _optional(dresidual, "dresidual", _BF16, (T, H), device)
-    guard, st = _launch(device, stream)
-    with guard:
-        dx = _output(dx, "dx", dy, (T, H), device)
-        dw = _output(dw, "dw", weight, (H,), device)
-        L = lib()
-        ws = _workspace(workspace, L.moe_rms_norm_backward_workspace_size(T, H), device)
-        _check(L.moe_rms_norm_backward(dy.data_ptr(), sp, w, r, dr, T, H, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
-                                       ws.numel(), st), "moe_rms_norm_backward")
+    and of the residual alike. ``stream``: launch there."""
+    shape, dev = _first(dy, "dy")
+    T, H = shape
+    sp = _tensor(s, "s", _BF16, shape, dev)
+    w = _tensor(weight, "weight", _BF16, (H,), dev)
+    r = _tensor(rstd, "rstd", _F32, (T,), dev)
+    dr = None if dresidual is None else _tensor(dresidual, "dresidual", _BF16, shape, dev)
+    dx = torch.empty_like(dy) if dx is None else dx
+    dw = torch.empty_like(weight) if dw is None else dw
+    dxp, dwp = _tensor(dx, "dx", _BF16, shape, dev), _tensor(dw, "dw", _BF16, (H,), dev)
+    L = lib()
+    ws = _workspace(workspace, L.moe_rms_norm_backward_workspace_size(T, H), dy)
+    _check(L.moe_rms_norm_backward(dy.data_ptr(), sp, w, r, dr, T, H, dxp, dwp, ws.data_ptr(), ws.numel(),
+                                   _current_stream(dev)), "moe_rms_norm_backward")
     return dx, dw
 
 
-def _gate_up_sizes(w_gate_up, H, device):
+def _gate_up(w_gate_up, H, dev):
+    """(I, address) of the [2I,H] weight."""
     _need(w_gate_up, "w_gate_up", (_BF16,), 2, cuda=False)
     twoI = w_gate_up.shape[0]
     if twoI % 2 != 0:
         raise ValueError(f"w_gate_up: {twoI} rows, expected 2*I (gate rows, then up rows)")
-    return twoI // 2, _tensor(w_gate_up, "w_gate_up", _BF16, (twoI, H), device)
+    return twoI // 2, _tensor(w_gate_up, "w_gate_up", _BF16, (twoI, H), dev)
 
 
-def gated_ffn(x, w_gate_up, act: str = "silu", save: bool = False, out=None, stream=None):
+@_operator
+def gated_ffn(x, w_gate_up, act: str = "silu", save: bool = False, out=None):
     """moe_gated_ffn: h = act(x Wg^T) * (x Wu^T) in one kernel, w_gate_up [2I,H]
     the gate rows and then the up rows (one expert's layout). Returns h bf16
     [T,I]; with save, (h, gu) with the fp32 pre-activations [T,2I] that
-    ``gated_ffn_backward`` takes."""
+    ``gated_ffn_backward`` takes. ``stream``: launch there."""
     a = _act(act, ACT)
-    T, H, device = _first(x, "x")
-    I, w = _gate_up_sizes(w_gate_up, H, device)
-    guard, st = _launch(device, stream)
-    with guard:
-        h = _output(out, "out", x, (T, I), device)
-        gu = torch.empty((T, 2 * I), dtype=_F32, device=device) if save else None
-        _check(lib().moe_gated_ffn(x.data_ptr(), w, T, H, I, a, h.data_ptr(), gu.data_ptr() if save else None, st),
-               "moe_gated_ffn")
+    (T, H), dev = _first(x, "x")
+    I, w = _gate_up(w_gate_up, H, dev)
+    h = x.new_empty((T, I)) if out is None else out
+    hp = _tensor(h, "out", _BF16, (T, I), dev)
+    gu = x.new_empty((T, 2 * I), dtype=_F32) if save else None
+    _check(lib().moe_gated_ffn(x.data_ptr(), w, T, H, I, a, hp, gu.data_ptr() if save else None,
+                               _current_stream(dev)), "moe_gated_ffn")
     return (h, gu) if save else h
 
 
-def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None, workspace=None, stream=None):
+@_operator
+def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None, workspace=None):
     """moe_gated_ffn_backward: (dx bf16 [T,H], dw bf16 [2I,H]) from dh [T,I], with
-    x, w_gate_up and the gu that the forward kept."""
+    x, w_gate_up and the gu that the forward kept. ``stream``: launch there."""
     a = _act(act, ACT)
-    T, H, device = _first(x, "x")
-    I, w = _gate_up_sizes(w_gate_up, H, device)
-    d = _tensor(dh, "dh", _BF16, (T, I), device)
-    g = _tensor(gu, "gu", _F32, (T, 2 * I), device)
-    guard, st = _launch(device, stream)
-    with guard:
-        dx = _output(dx, "dx", x, (T, H), device)
-        dw = _output(dw, "dw", w_gate_up, (2 * I, H), device)
-        L = lib()
-        ws = _workspace(workspace, L.moe_gated_ffn_backward_workspace_size(T, I), device)
-        _check(L.moe_gated_ffn_backward(d, x.data_ptr(), w, g, T, H, I, a, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
-                                        ws.numel(), st), "moe_gated_ffn_backward")
+    shape, dev = _first(x, "x")
+    T, H = shape
+    I, w = _gate_up(w_gate_up, H, dev)
+    d = _tensor(dh, "dh", _BF16, (T, I), dev)
+    g = _tensor(gu, "gu", _F32, (T, 2 * I), dev)
+    dx = torch.empty_like(x) if dx is None else dx
+    dw = torch.empty_like(w_gate_up) if dw is None else dw
+    dxp, dwp = _tensor(dx, "dx", _BF16, shape, dev), _tensor(dw, "dw", _BF16, (2 * I, H), dev)
+    L = lib()
+    ws = _workspace(workspace, L.moe_gated_ffn_backward_workspace_size(T, I), x)
+    _check(L.moe_gated_ffn_backward(d, x.data_ptr(), w, g, T, H, I, a, dxp, dwp, ws.data_ptr(), ws.numel(),
+                                    _current_stream(dev)), "moe_gated_ffn_backward")
     return dx, dw
 
 
-def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False, out=None, stream=None):
+@_operator
+def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False, out=None):
     """moe_linear: y = act(x W^T + bias) + residual, w [N,K], rounded once. ``out``
     may be residual. Returns y bf16 [T,N]; with save, (y, z) with the fp32
     pre-activation [T,N] that ``linear_backward`` takes (None without an
-    activation: the backward pass needs none)."""
+    activation: the backward pass needs none). ``stream``: launch there."""
     a = _act(act, _LINEAR_ACT)
-    T, K, device = _first(x, "x")
+    (T, K), dev = _first(x, "x")
     _need(w, "w", (_BF16,), 2, cuda=False)
     N = w.shape[0]
-    wp = _tensor(w, "w", _BF16, (N, K), device)
-    b = _optional(bias, "bias", _BF16, (N,), device)
-    r = _optional(residual, "residual", _BF16, (T, N), device)
-    guard, st = _launch(device, stream)
-    with guard:
-        y = _output(out, "out", x, (T, N), device)
-        z = torch.empty((T, N), dtype=_F32, device=device) if save and act != "none" else None
-        _check(lib().moe_linear(x.data_ptr(), wp, b, r, T, K, N, a, y.data_ptr(),
-                                None if z is None else z.data_ptr(), st), "moe_linear")
+    wp = _tensor(w, "w", _BF16, (N, K), dev)
+    b = None if bias is None else _tensor(bias, "bias", _BF16, (N,), dev)
+    r = None if residual is None else _tensor(residual, "residual", _BF16, (T, N), dev)
+    y = x.new_empty((T, N)) if out is None else out
+    yp = _tensor(y, "out", _BF16, (T, N), dev)
+    z = x.new_empty((T, N), dtype=_F32) if save and act != "none" else None
+    _check(lib().moe_linear(x.data_ptr(), wp, b, r, T, K, N, a, yp, None if z is None else z.data_ptr(),
+                            _current_stream(dev)), "moe_linear")
     return (y, z) if save else y
 
 
-def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=None, dw=None, workspace=None,
-                    stream=None):
+@_operator
+def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=None, dw=None, workspace=None):
     """moe_linear_backward: (dx bf16 [T,K], dw bf16 [N,K], db bf16 [N] or None)
     from dy [T,N], with x, w and, for an activation, the z that the forward
-    kept. ``bias`` asks for db; the residual's gradient is dy itself."""
+    kept. ``bias`` asks for db; the residual's gradient is dy itself.
+    ``stream``: launch there."""
     a = _act(act, _LINEAR_ACT)
-    T, K, device = _first(x, "x")
+    shape, dev = _first(x, "x")
+    T, K = shape
     _need(w, "w", (_BF16,), 2, cuda=False)
     N = w.shape[0]
-    wp = _tensor(w, "w", _BF16, (N, K), device)
-    d = _tensor(dy, "dy", _BF16, (T, N), device)
-    zp = _optional(z, "z", _F32, (T, N), device)
-    guard, st = _launch(device, stream)
-    with guard:
-        dx = _output(dx, "dx", x, (T, K), device)
-        dw = _output(dw, "dw", w, (N, K), device)
-        db = torch.empty((N,), dtype=_BF16, device=device) if bias else None
-        L = lib()
-        ws = _workspace(workspace, L.moe_linear_backward_workspace_size(T, N, a, int(bool(bias))), device)
-        _check(L.moe_linear_backward(d, x.data_ptr(), wp, zp, T, K, N, a, dx.data_ptr(), dw.data_ptr(),
-                                     None if db is None else db.data_ptr(), ws.data_ptr(), ws.numel(), st),
-               "moe_linear_backward")
+    wp = _tensor(w, "w", _BF16, (N, K), dev)
+    d = _tensor(dy, "dy", _BF16, (T, N), dev)
+    zp = None if z is None else _tensor(z, "z", _F32, (T, N), dev)
+    dx = torch.empty_like(x) if dx is None else dx
+    dw = torch.empty_like(w) if dw is None else dw
+    dxp, dwp = _tensor(dx, "dx", _BF16, shape, dev), _tensor(dw, "dw", _BF16, (N, K), dev)
+    db = w.new_empty(N) if bias else None
+    L = lib()
+    ws = _workspace(workspace, L.moe_linear_backward_workspace_size(T, N, a, int(bool(bias))), x)
+    _check(L.moe_linear_backward(d, x.data_ptr(), wp, zp, T, K, N, a, dxp, dwp, None if db is None else db.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), _current_stream(dev)), "moe_linear_backward")
     return dx, dw, db
