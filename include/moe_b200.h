@@ -175,6 +175,19 @@ moe_status moe_forward(const moe_shape* shape, const void* x, const int32_t* top
                        const uint8_t* sw_gate_up, const uint8_t* sw_down, void* out,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * moe_forward_quantized -- moe_forward of e4m3 experts on activations that are
+ * quantised already, as moe_rms_norm gives them: x_codes e4m3 [T, H] (16-byte
+ * aligned) and x_scales fp32 [T, H/128], value = code * scale. The permute stage
+ * copies them instead of reading bf16 rows and quantising; everything after it
+ * is moe_forward, so codes and scales equal to the ones it forms from x give
+ * the same bits. MOE_ERR_UNSUPPORTED for other expert types.
+ */
+moe_status moe_forward_quantized(const moe_shape* shape, const uint8_t* x_codes, const float* x_scales,
+                                 const int32_t* topk_idx, const float* topk_w, const void* w_gate_up,
+                                 const void* w_down, const uint8_t* sw_gate_up, const uint8_t* sw_down, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* moe_forward that also records caller-created CUDA events (cudaEvent_t passed
  * as void*) between its stages, on `stream`: events[0] before the permute,
  * [1] after it, [2] after the gate/up stage, [3] after the down stage, [4]

@@ -32,7 +32,7 @@ EXPORTS = ["moe_route", "moe_workspace_size", "moe_forward", "moe_forward_timed"
            "moe_set_test_hooks", "moe_router", "moe_forward_noalloc_status",
            "moe_rms_norm", "moe_rms_norm_backward", "moe_rms_norm_backward_workspace_size",
            "moe_gated_ffn", "moe_gated_ffn_backward", "moe_gated_ffn_backward_workspace_size",
-           "moe_linear", "moe_linear_backward", "moe_linear_backward_workspace_size"]
+           "moe_linear", "moe_linear_backward", "moe_linear_backward_workspace_size", "moe_forward_quantized"]
 
 
 class MoeError(RuntimeError):
@@ -73,6 +73,8 @@ def lib() -> ctypes.CDLL:
         L.moe_forward.restype = i32
         L.moe_forward_timed.argtypes = fwd + [ctypes.POINTER(vp), i32]
         L.moe_forward_timed.restype = i32
+        L.moe_forward_quantized.argtypes = [ctypes.POINTER(MoeShape), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_forward_quantized.restype = i32
         L.moe_workspace_query.argtypes = [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWorkspaceLayout)]
         L.moe_workspace_query.restype = i32
         L.moe_read_device_status.argtypes = [vp, vp]
@@ -198,13 +200,14 @@ def route(logits: torch.Tensor, k: int, topk_idx: torch.Tensor | None = None, to
     return topk_idx, topk_w
 
 
-def _check_forward_args(x, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up, sw_down, out, workspace=None):
+def _check_forward_args(x, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up, sw_down, out, workspace=None,
+                        x_dtype=torch.bfloat16):
     """Checks every tensor of a forward call against the layer the weights
     define (E experts, [gate; up] rows 2I, hidden H, top-k from topk_idx) and
     returns (T, H, I, E, k, wdtype). Sizes first, then that all share x's CUDA
     device: nothing reaches the library unless every pointer covers the
     extent the kernels will read or write."""
-    _need(x, "x", (torch.bfloat16,), 2, cuda=False)
+    _need(x, "x", (x_dtype,), 2, cuda=False)
     T, H = x.shape
     _need(topk_idx, "topk_idx", (torch.int32,), 2, cuda=False)
     k = topk_idx.shape[1]
@@ -266,6 +269,31 @@ def forward(x, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up=None, sw_down=Non
                     e.record(st)
             ev = (ctypes.c_void_p * len(events))(*[e.cuda_event for e in events])
             _check(lib().moe_forward_timed(*args, ev, len(events)), "moe_forward_timed")
+    return out, workspace
+
+
+def forward_quantized(codes, scales, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up, sw_down, out=None,
+                      workspace=None, path="auto", stream=None, act="silu"):
+    """moe_forward_quantized: forward of e4m3 experts on activations quantised
+    already (``rms_norm(..., quantize=True)``): codes float8_e4m3fn [T,H], scales
+    fp32 [T,H/128]. Returns (out bf16 [T,H], workspace)."""
+    _need(codes, "codes", (_FLOAT8,), 2, cuda=False)
+    _need(scales, "scales", (torch.float32,), 2, (codes.shape[0], codes.shape[1] // 128), cuda=False)
+    if w_gate_up.dtype != _FLOAT8:
+        raise ValueError(f"quantised activations need e4m3 experts, these are {w_gate_up.dtype}")
+    T, H, I, E, k, wdtype = _check_forward_args(codes, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up, sw_down, out,
+                                                workspace, _FLOAT8)
+    _same_device(codes.device, scales=scales)
+    shape = make_shape(T, H, I, E, k, wdtype, path, act)
+    with torch.cuda.device(codes.device):
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=codes.device)
+        if workspace is None:
+            workspace = alloc_workspace(shape, codes.device)
+        _check(lib().moe_forward_quantized(ctypes.byref(shape), _ptr(codes), _ptr(scales), _ptr(topk_idx), _ptr(topk_w),
+                                           _ptr(w_gate_up), _ptr(w_down), _ptr(sw_gate_up), _ptr(sw_down), _ptr(out),
+                                           _ptr(workspace), workspace.numel(), _stream(stream, codes.device)),
+               "moe_forward_quantized")
     return out, workspace
 
 
@@ -361,6 +389,42 @@ class MoELayer:
                          workspace=self._workspace(x.shape[0], x.device), path=self.path, events=events,
                          act=self.act)
         return out
+
+
+class MoEBlock:
+    """The feed-forward half of a transformer layer: the residual's addition and
+    the RMS norm, the router, the routed experts of ``layer`` and, if given, a
+    shared expert that every token passes (gate_up [2I,H] and down [H,I], bf16,
+    the layer's activation), whose projection back adds the routed sum:
+
+        s = x + residual,  n = norm(s),  y = experts(n) + shared(n)
+
+    ``block(x, residual)`` returns (y, s), both bf16 [T,H]: the next norm's x and
+    residual. e4m3 experts take the norm's codes and scales. Calls share the
+    layer's workspace: order them, for example on one stream."""
+
+    def __init__(self, layer: "MoELayer", w_norm, w_router, shared_gate_up=None, shared_down=None,
+                 eps: float = 1e-6):
+        if (shared_gate_up is None) != (shared_down is None):
+            raise ValueError("a shared expert needs both shared_gate_up and shared_down")
+        self.layer, self.w_norm, self.w_router = layer, w_norm, w_router
+        self.shared_gate_up, self.shared_down, self.eps = shared_gate_up, shared_down, float(eps)
+
+    def __call__(self, x, residual=None):
+        layer = self.layer
+        n = rms_norm(x, self.w_norm, residual=residual, eps=self.eps, quantize=layer.w_gate_up.dtype == _FLOAT8)
+        idx, w = router(n.y, self.w_router, layer.k)
+        ws = layer._workspace(x.shape[0], x.device)
+        if n.codes is not None:
+            y, _ = forward_quantized(n.codes, n.scales, idx, w, layer.w_gate_up, layer.w_down, layer.sw_gate_up,
+                                     layer.sw_down, workspace=ws, path=layer.path, act=layer.act)
+        else:
+            y, _ = forward(n.y, idx, w, layer.w_gate_up, layer.w_down, layer.sw_gate_up, layer.sw_down, workspace=ws,
+                           path=layer.path, act=layer.act)
+        if self.shared_gate_up is not None:
+            h = gated_ffn(n.y, self.shared_gate_up, act=layer.act)
+            y = linear(h, self.shared_down, residual=y, out=y)
+        return y, n.residual
 
 
 class MoEGraph:
@@ -468,4 +532,4 @@ class MoEPipeline:
 __all__ = ["lib", "route", "forward", "forward_noalloc", "noalloc_device_status", "MoEGraph", "MoEPipeline", "workspace_size", "workspace_layout", "alloc_workspace",
            "read_device_status", "set_test_hooks", "router", "make_shape", "MoELayer", "MoeError", "MoeShape", "EXPORTS", "STATUS",
            "status_string", "PATH", "WDTYPE", "ACT", "rms_norm", "rms_norm_backward", "RMSNormOutput", "gated_ffn",
-           "gated_ffn_backward", "linear", "linear_backward"]
+           "gated_ffn_backward", "linear", "linear_backward", "forward_quantized", "MoEBlock"]

@@ -236,7 +236,8 @@ bool bf16_64_not_128(const moe_shape* s) {
 moe_status forward_impl(const moe_shape* shape, const void* x, const int32_t* topk_idx, const float* topk_w,
                         const void* w_gate_up, const void* w_down, const uint8_t* sw_gate_up,
                         const uint8_t* sw_down, void* out, void* workspace, size_t workspace_bytes, void* stream,
-                        void* const* events, int32_t n_events) {
+                        void* const* events, int32_t n_events, const uint8_t* x_codes = nullptr,
+                        const float* x_scales = nullptr) {
   if (bf16_64_not_128(shape)) return MOE_ERR_UNSUPPORTED;
   if (!validate_shape(shape)) return MOE_ERR_INVALID_ARG;
   if (!(n_events == 0 || (n_events == 5 && events != nullptr))) return MOE_ERR_INVALID_ARG;
@@ -253,7 +254,8 @@ moe_status forward_impl(const moe_shape* shape, const void* x, const int32_t* to
     return MOE_ERR_UNSUPPORTED;
   if (plan.path == MOE_PATH_FUSED && !fused_supported(shape)) return MOE_ERR_UNSUPPORTED;
   if (shape->T == 0) return MOE_OK;
-  if (x == nullptr || topk_idx == nullptr || topk_w == nullptr || w_gate_up == nullptr || w_down == nullptr ||
+  const bool quantised = x_codes != nullptr;  // x comes as e4m3 codes and scales (checked by the entry point)
+  if ((!quantised && x == nullptr) || topk_idx == nullptr || topk_w == nullptr || w_gate_up == nullptr || w_down == nullptr ||
       out == nullptr || workspace == nullptr)
     return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w_gate_up, 16) || !aligned(w_down, 16) ||
@@ -277,7 +279,7 @@ moe_status forward_impl(const moe_shape* shape, const void* x, const int32_t* to
       return MOE_ERR_CUDA;
     return mark(2) && mark(3) && mark(4) ? MOE_OK : MOE_ERR_CUDA;
   }
-  if (launch_permute(shape, plan, topk_idx, x, ws, st) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launch_permute(shape, plan, topk_idx, x, x_codes, x_scales, ws, st) != cudaSuccess) return MOE_ERR_CUDA;
   if (!mark(1)) return MOE_ERR_CUDA;
   cudaError_t err;
   if (plan.path == MOE_PATH_DECODE && fp4) {
@@ -351,6 +353,18 @@ moe_status moe_forward_timed(const moe_shape* shape, const void* x, const int32_
                              void* stream, void* const* events, int32_t n_events) {
   return forward_impl(shape, x, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up, sw_down, out, workspace,
                       workspace_bytes, stream, events, n_events);
+}
+
+moe_status moe_forward_quantized(const moe_shape* shape, const uint8_t* x_codes, const float* x_scales,
+                                 const int32_t* topk_idx, const float* topk_w, const void* w_gate_up,
+                                 const void* w_down, const uint8_t* sw_gate_up, const uint8_t* sw_down, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!validate_shape(shape)) return MOE_ERR_INVALID_ARG;
+  if (shape->wdtype != MOE_DT_E4M3) return MOE_ERR_UNSUPPORTED;
+  if (shape->T > 0 && (x_codes == nullptr || x_scales == nullptr || !aligned(x_codes, 16) || !aligned(x_scales, 4)))
+    return MOE_ERR_INVALID_ARG;
+  return forward_impl(shape, nullptr, topk_idx, topk_w, w_gate_up, w_down, sw_gate_up, sw_down, out, workspace,
+                      workspace_bytes, stream, nullptr, 0, x_codes, x_scales);
 }
 
 moe_status moe_workspace_query(const moe_shape* shape, moe_workspace_layout* layout) {

@@ -57,8 +57,9 @@ cudaError_t launch_route(const float* logits, int T, int E, int k, int* idx, flo
 cudaError_t launch_router(const void* x, const void* w_router, int T, int H, int E, int k, float* logits, int* idx,
                           float* w, cudaStream_t st);
 
-cudaError_t launch_permute(const moe_shape* s, const Plan& p, const int* topk_idx, const void* x, uint8_t* ws,
-                           cudaStream_t st);
+// x bf16, or (e4m3 experts) x null and its codes and group scales given.
+cudaError_t launch_permute(const moe_shape* s, const Plan& p, const int* topk_idx, const void* x,
+                           const uint8_t* x_codes, const float* x_scales, uint8_t* ws, cudaStream_t st);
 
 cudaError_t launch_gemm_bf16(const moe_shape* s, const Plan& p, const void* w_gate_up, const void* w_down,
                              uint8_t* ws, int which, int num_sms, cudaStream_t st);

@@ -202,13 +202,36 @@ __device__ __forceinline__ void quant_group_e4m3(const uint4& v, unsigned hmask,
   if (l16 == 0) *scale = sc;
 }
 
-// Quantise one token's row into permuted row `row` (one warp; each half-warp
-// owns one group at a time).
-__device__ __forceinline__ void quant_row_e4m3(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ xq,
-                                               float* __restrict__ xs, int t, int row, int H, int lane) {
+// Activations that come quantised already: codes e4m3 [T, H] and scales fp32
+// [T, H/128], or null for bf16 rows that the permute stage quantises.
+struct Quantised {
+  const uint8_t* codes;
+  const float* scales;
+};
+
+// Lane l16's eight codes of group g of token t, and the group's scale.
+__device__ __forceinline__ uint2 load_group_codes(const Quantised& q, long long t, int g, int l16, int H, float* sc) {
+  *sc = __ldg(q.scales + static_cast<size_t>(t) * (H / 128) + g);
+  return __ldg(reinterpret_cast<const uint2*>(q.codes + static_cast<size_t>(t) * H + g * 128) + l16);
+}
+
+// Quantise one token's row into permuted row `row`, or copy it there when it
+// is quantised (one warp; each half-warp owns one group at a time).
+__device__ __forceinline__ void quant_row_e4m3(const __nv_bfloat16* __restrict__ x, const Quantised& qx,
+                                               uint8_t* __restrict__ xq, float* __restrict__ xs, int t, int row, int H,
+                                               int lane) {
   const int half = lane >> 4, l16 = lane & 15;
   const unsigned hmask = 0xFFFFu << (16 * half);
   const int G = H / 128;
+  if (qx.codes != nullptr) {
+    for (int g = half; g < G; g += 2) {
+      float sc;
+      const uint2 codes = load_group_codes(qx, t, g, l16, H, &sc);
+      reinterpret_cast<uint2*>(xq + static_cast<size_t>(row) * H + g * 128)[l16] = codes;
+      if (l16 == 0) xs[static_cast<size_t>(row) * G + g] = sc;
+    }
+    return;
+  }
   const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * H);
   for (int g = half; g < G; g += 2)
     quant_group_e4m3(__ldg(src + g * 16 + l16), hmask, l16,
@@ -222,7 +245,7 @@ __device__ __forceinline__ void quant_row_e4m3(const __nv_bfloat16* __restrict__
 // With slot_row the sources are assignments a (token a / k, destination row
 // slot_row[a], skipped when negative); without it they are tokens, each
 // written once to row t (the e4m3 DECODE path reads x per token).
-__global__ void __launch_bounds__(256) stage_rows_kernel(const __nv_bfloat16* __restrict__ x,
+__global__ void __launch_bounds__(256) stage_rows_kernel(const __nv_bfloat16* __restrict__ x, const Quantised qx,
                                                          const int* __restrict__ slot_row, long long n_src, int k,
                                                          int H, __nv_bfloat16* __restrict__ xa,
                                                          uint8_t* __restrict__ xq, float* __restrict__ xs) {
@@ -243,6 +266,13 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(const __nv_bfloat16* __
       t = a / k;
       if (row < 0) continue;  // the whole half-warp skips together
     }
+    if (qx.codes != nullptr) {
+      float sc;
+      const uint2 codes = load_group_codes(qx, t, g, l16, H, &sc);
+      reinterpret_cast<uint2*>(xq + static_cast<size_t>(row) * H + g * 128)[l16] = codes;
+      if (l16 == 0) xs[static_cast<size_t>(row) * G + g] = sc;
+      continue;
+    }
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * H + g * 128) + l16);
     if (xa != nullptr)
       reinterpret_cast<uint4*>(xa + static_cast<size_t>(row) * H + g * 128)[l16] = v;
@@ -262,7 +292,7 @@ __global__ void __launch_bounds__(256) permute_scatter_kernel(const int* __restr
                                                               const int* __restrict__ local_rank,
                                                               const int* __restrict__ mt_base,
                                                               int* __restrict__ row_src, int* __restrict__ slot_row,
-                                                              const __nv_bfloat16* __restrict__ x,
+                                                              const __nv_bfloat16* __restrict__ x, const Quantised qx,
                                                               __nv_bfloat16* __restrict__ xa, uint8_t* __restrict__ xq,
                                                               float* __restrict__ xs, int H) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
@@ -305,14 +335,15 @@ __global__ void __launch_bounds__(256) permute_scatter_kernel(const int* __restr
     if (xq != nullptr) {
       // both half-warps run the same number of iterations (G rounded up to
       // even), so the full-warp row broadcasts below stay converged
-      uint4 vn = half < G ? __ldg(src + half * 16 + l16) : make_uint4(0u, 0u, 0u, 0u);
+      const bool quantised = qx.codes != nullptr;
+      uint4 vn = !quantised && half < G ? __ldg(src + half * 16 + l16) : make_uint4(0u, 0u, 0u, 0u);
       for (int g0 = 0; g0 < G; g0 += 2) {
         const int g = g0 + half;
         const uint4 v = vn;  // the next group's load is in flight while this one is quantised
-        if (g + 2 < G) vn = __ldg(src + (g + 2) * 16 + l16);
+        if (!quantised && g + 2 < G) vn = __ldg(src + (g + 2) * 16 + l16);
         uint2 codes = make_uint2(0u, 0u);
         float sc = 1.f;
-        if (g < G) codes = quant_group_codes(v, hmask, &sc);
+        if (g < G) codes = quantised ? load_group_codes(qx, t, g, l16, H, &sc) : quant_group_codes(v, hmask, &sc);
         for (int j = 0; j < nj; ++j) {
           const int r = __shfl_sync(0xffffffffu, row, j);
           if (r >= 0 && g < G) {
@@ -332,7 +363,7 @@ __global__ void __launch_bounds__(1024) permute_small_kernel(const int* __restri
                                                              int* __restrict__ touched, int* __restrict__ hdr,
                                                              int* __restrict__ row_src, int* __restrict__ slot_row,
                                                              int* __restrict__ local_rank, int* dev_status,
-                                                             const __nv_bfloat16* __restrict__ x,
+                                                             const __nv_bfloat16* __restrict__ x, const Quantised qx,
                                                              __nv_bfloat16* __restrict__ xa, uint8_t* __restrict__ xq,
                                                              float* __restrict__ xs, int H) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
@@ -397,14 +428,15 @@ __global__ void __launch_bounds__(1024) permute_small_kernel(const int* __restri
       slot_row[a] = row;
     }
     if (xa != nullptr) copy_row_bf16(x, xa, a / k, row, H, lane);
-    if (xq != nullptr) quant_row_e4m3(x, xq, xs, a / k, row, H, lane);
+    if (xq != nullptr) quant_row_e4m3(x, qx, xq, xs, a / k, row, H, lane);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_permute(const moe_shape* s, const Plan& p, const int* topk_idx, const void* x, uint8_t* ws,
-                           cudaStream_t st) {
+cudaError_t launch_permute(const moe_shape* s, const Plan& p, const int* topk_idx, const void* x,
+                           const uint8_t* x_codes, const float* x_scales, uint8_t* ws, cudaStream_t st) {
+  const Quantised qx{x_codes, x_scales};
   const int T = s->T, k = s->k, E = s->E, H = s->H;
   int* status = reinterpret_cast<int*>(ws + p.status);
   int* hdr = reinterpret_cast<int*>(ws + p.hdr);
@@ -437,14 +469,14 @@ cudaError_t launch_permute(const moe_shape* s, const Plan& p, const int* topk_id
     const long long want = (tasks + 15) / 16;  // blocks of 16 half-warps
     const long long cap = static_cast<long long>(device_sm_count()) * 8;
     const unsigned grid = static_cast<unsigned>(std::max<long long>(1, std::min(want, cap)));
-    return launch_pdl(stage_rows_kernel, dim3(grid), dim3(256), 0, st, xb, slots, n_src, k, H, xa, xq, xs);
+    return launch_pdl(stage_rows_kernel, dim3(grid), dim3(256), 0, st, xb, qx, slots, n_src, k, H, xa, xq, xs);
   };
 
   cudaError_t err = cudaMemsetAsync(status, 0, kStatusWordsZeroed * sizeof(int), st);
   if (err != cudaSuccess) return err;
   if (T <= kSmallPermuteT) {
     err = launch_pdl(permute_small_kernel, dim3(1), dim3(1024), mask_bytes, st, topk_idx, T, k, E, p.bm, cnt, mt_base,
-                     pt_base, touched, hdr, row_src, slot_row, lrank, status, xb, stage_in_small ? xa : nullptr,
+                     pt_base, touched, hdr, row_src, slot_row, lrank, status, xb, qx, stage_in_small ? xa : nullptr,
                      stage_in_small ? xq : nullptr, stage_in_small ? xs : nullptr, H);
     if (err != cudaSuccess) return err;
     if (stage_in_small || (!prefill && !fp8 && !copy_x)) return cudaSuccess;
@@ -457,7 +489,7 @@ cudaError_t launch_permute(const moe_shape* s, const Plan& p, const int* topk_id
                    touched, hdr, row_src);
   if (err != cudaSuccess) return err;
   err = launch_pdl(permute_scatter_kernel, dim3(static_cast<unsigned>((T + 7) / 8)), dim3(256), 0, st, topk_idx, T, k,
-                   E, p.bm, counts, lrank, mt_base, row_src, slot_row, xb, xa, prefill ? xq : nullptr,
+                   E, p.bm, counts, lrank, mt_base, row_src, slot_row, xb, qx, xa, prefill ? xq : nullptr,
                    prefill ? xs : nullptr, H);
   if (err != cudaSuccess) return err;
   return (!prefill && fp8) ? stage(nullptr, T) : cudaSuccess;

@@ -140,3 +140,42 @@ def test_binding_refuses_what_the_library_cannot_see():
         moe.gated_ffn(x, wg, act="none")
     with pytest.raises(ValueError, match="act"):
         moe.linear(x, wl, act="tanh")
+
+
+def test_quantized_forward_refusals(L):
+    """moe_forward_quantized takes e4m3 experts only, and needs codes and scales."""
+    import ctypes
+
+    args = [at(i) for i in range(1, 10)]
+
+    def run(s, codes, scales, need=1 << 40):
+        return L.moe_forward_quantized(ctypes.byref(s), codes, scales, *args[2:8], at(20), at(21), need, None)
+
+    s = moe.make_shape(4, 256, 256, 8, 2, "e4m3")
+    assert run(s, None, at(1)) == BAD and run(s, at(0), None) == BAD
+    assert run(s, at(0) + 8, at(1)) == BAD and run(s, at(0), at(1) + 2) == BAD
+    assert run(s, at(0), at(1), 16) == SPACE
+    for other in ("bf16", "e2m1"):
+        assert run(moe.make_shape(4, 256, 256, 8, 2, other), at(0), at(1)) == -2
+    assert run(moe.make_shape(4, 100, 256, 8, 2, "e4m3"), at(0), at(1)) == BAD
+    assert run(moe.make_shape(0, 256, 256, 8, 2, "e4m3"), None, None) == 0
+
+
+def test_block_and_quantized_binding_refusals():
+    f8 = torch.float8_e4m3fn
+    T, H, I, E, k = 4, 256, 256, 8, 2
+    idx, w = torch.zeros((T, k), dtype=torch.int32), torch.zeros((T, k))
+    ok = dict(codes=torch.zeros((T, H), dtype=f8), scales=torch.zeros((T, H // 128)), topk_idx=idx, topk_w=w,
+              w_gate_up=torch.zeros((E, 2 * I, H), dtype=f8), w_down=torch.zeros((E, H, I), dtype=f8),
+              sw_gate_up=torch.zeros((E, 2 * I // 128, H // 128), dtype=torch.uint8),
+              sw_down=torch.zeros((E, H // 128, I // 128), dtype=torch.uint8))
+    for bad, msg in ((dict(codes=torch.zeros((T, H), dtype=BF)), "codes: dtype"),
+                     (dict(scales=torch.zeros((T, H // 128 + 1))), "scales: shape"),
+                     (dict(w_gate_up=torch.zeros((E, 2 * I, H), dtype=BF), w_down=torch.zeros((E, H, I), dtype=BF),
+                           sw_gate_up=None, sw_down=None), "need e4m3 experts"),
+                     (dict(), "CUDA device")):
+        with pytest.raises(ValueError, match=msg):
+            moe.forward_quantized(**dict(ok, **bad))
+    layer = moe.MoELayer(ok["w_gate_up"], ok["w_down"], k)
+    with pytest.raises(ValueError, match="both shared_gate_up and shared_down"):
+        moe.MoEBlock(layer, torch.ones(H, dtype=BF), torch.zeros((E, H), dtype=BF), shared_down=torch.zeros((H, I)))
