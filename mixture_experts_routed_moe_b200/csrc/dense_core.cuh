@@ -28,6 +28,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, status, limit_ns));
 }
 
+// The two halves of cluster_sync, and a store into another CTA's shared memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
 // Shared-memory descriptor of an MN-major operand (its rows along K, 64
 // consecutive M or N elements per 128-byte row) stored by TMA boxes of
 // 64 elements x 64 K rows with the 128-byte swizzle: 8-row atoms of 1024 bytes

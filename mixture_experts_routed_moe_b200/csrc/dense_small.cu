@@ -10,17 +10,23 @@
 // pass, where W^T's rows are the outputs). A unit is up to 128 weight rows
 // (gated: as many gate rows as up rows); a cluster of C CTAs owns a unit, CTA r
 // taking the r-th of C ranges of K through a TMA ring into one TMEM
-// accumulator of 128 x n_pad. Afterwards the ring is free: each CTA puts its
-// partial into shared memory, token by token, and after a cluster barrier
-// the CTAs share out the unit's outputs: the C partials are read through
-// distributed shared memory and added in rank order (one fixed order:
-// deterministic, no atomics), the epilogue is applied in fp32.
+// accumulator of 128 x n_pad. The CTAs share out the unit's outputs, each adding
+// the C partials of its part in rank order (one fixed order: deterministic, no
+// atomics) and applying the epilogue in fp32. How the partials travel:
+//   push  (token tiles of at most 64): each CTA stores its partial, row by row,
+//         straight from TMEM into the shared memory of the CTA that adds it, in
+//         a region of its own; one cluster barrier, and all reads are local
+//   pull  (wider tiles, whose region would take the ring's room): the partial
+//         goes to the CTA's own ring, which is free by then, and is read through
+//         distributed shared memory between two cluster barriers
+// From the last MMA to the end pull takes 3.1 us, push 1.7 (16 x 2048 -> 7168).
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 TMEM to shared memory, then all
 // eight reduce. Every wait is bounded; a cluster with a wait that gave up
 // writes NaN.
 #include <algorithm>
 #include <limits>
+#include <type_traits>
 
 #include "dense_core.cuh"
 
@@ -49,11 +55,17 @@ struct SmallParams {
   unsigned long long timeout_ns;
 };
 
-// Bytes of the ring: half an SM's shared memory (two CTAs of it, or one and the
-// next kernel's, which starts early). The partial of a token tile fits it.
-constexpr int kRing = 98304;
-static_assert(kTileTokens * kLd * 4 <= kRing, "the partial rows reuse the ring");
-size_t small_smem() { return 1024 + static_cast<size_t>(kRing) + (2 * kMaxStages + 1) * 8 + 32; }
+// A CTA takes half an SM's shared memory (two CTAs of it, or one and the next
+// kernel's, which starts early): the ring, and for push the partials' region.
+constexpr int kSmemBytes = 114688;
+constexpr int kSlack = 1024, kBarrierBytes = 512;
+constexpr int kPushTokens = 64;  // most tokens of a token tile that is pushed
+static_assert(kTileTokens * kLd * 4 <= kSmemBytes - kSlack - kBarrierBytes, "the partial rows reuse the ring");
+__host__ __device__ constexpr int region_bytes(int tile_t, bool push) { return push ? tile_t * kTileM * 4 : 0; }
+int ring_stages(int tile_t, int n_pad, bool push) {
+  const int ring = kSmemBytes - kSlack - kBarrierBytes - region_bytes(tile_t, push);
+  return std::min(kMaxStages, ring / (kA + n_pad * kBK * 2));
+}
 
 // The C partials at one place, added in rank order; all loads are in flight together.
 template <int kC>
@@ -71,67 +83,111 @@ __device__ __forceinline__ float4 sum_ranks(uint32_t addr) {
   return v[0];
 }
 
-// This CTA's share of the unit's outputs, four consecutive ones of a token per step.
+// Four consecutive outputs of one token, from their sums: bias, activation,
+// residual, the one rounding. `res` and `bias` are the four values' inputs.
+template <bool kGated>
+__device__ __forceinline__ void write_outputs(const SmallParams& p, float4 z, float4 u, uint2 bias, uint2 res, int t,
+                                              int n, bool aborted) {
+  const size_t at = static_cast<size_t>(t) * p.N + n;
+  float v[4];
+  if (!kGated && p.bias != nullptr) {
+    z.x += bf16_lo(bias.x);
+    z.y += bf16_hi(bias.x);
+    z.z += bf16_lo(bias.y);
+    z.w += bf16_hi(bias.y);
+  }
+  if (p.save != nullptr) {
+    float* s = p.save + (kGated ? 2 * static_cast<size_t>(t) * p.N + n : at);
+    *reinterpret_cast<float4*>(s) = z;
+    if (kGated) *reinterpret_cast<float4*>(s + p.N) = u;
+  }
+  with_act(p.act, [&](auto tag) {
+    constexpr int kAct = decltype(tag)::value;
+    v[0] = act_t<kAct>(z.x);
+    v[1] = act_t<kAct>(z.y);
+    v[2] = act_t<kAct>(z.z);
+    v[3] = act_t<kAct>(z.w);
+  });
+  if (kGated) {
+    v[0] *= u.x;
+    v[1] *= u.y;
+    v[2] *= u.z;
+    v[3] *= u.w;
+  } else if (p.residual != nullptr) {
+    v[0] += bf16_lo(res.x);
+    v[1] += bf16_hi(res.x);
+    v[2] += bf16_lo(res.y);
+    v[3] += bf16_hi(res.y);
+  }
+  uint2 o = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  if (aborted) o = make_uint2(0x7FC07FC0u, 0x7FC07FC0u);
+  *reinterpret_cast<uint2*>(p.out + at) = o;
+}
+
+// The bias and the residual of four outputs.
+__device__ __forceinline__ void load_addends(const SmallParams& p, int t, int n, uint2& bias, uint2& res) {
+  bias = res = make_uint2(0u, 0u);
+  if (n >= p.N) return;
+  if (p.bias != nullptr) bias = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+  if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + static_cast<size_t>(t) * p.N + n);
+}
+
+// Pull: this CTA's share of the unit's outputs, the partials read from their CTAs.
 template <bool kGated, int kC>
-__device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
-                                       bool aborted) {
+__device__ __forceinline__ void finish_pull(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
+                                            bool aborted) {
   const int per = p.rows / 4;
   const int items = nt * per;
   for (int i = rank * items / kC + threadIdx.x; i < (rank + 1) * items / kC; i += kThreads) {
     const int t = i / per, r = (i - t * per) * 4;
     const int n = n0 + r;
     if (n >= p.N) continue;  // N is a multiple of 8
-    float v[4];
-    const size_t at = static_cast<size_t>(t0 + t) * p.N + n;
+    uint2 bias, res;
+    if (!kGated) load_addends(p, t0 + t, n, bias, res);
     const uint32_t sp = smem_u32(s_part + t * kLd + r);
-    if (aborted) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = __int_as_float(0x7FC00000);
-    } else if (kGated) {
-      const float4 g = sum_ranks<kC>(sp), u = sum_ranks<kC>(sp + p.rows * 4);
-      if (p.save != nullptr) {
-        float* s = p.save + 2 * static_cast<size_t>(t0 + t) * p.N + n;
-        *reinterpret_cast<float4*>(s) = g;
-        *reinterpret_cast<float4*>(s + p.N) = u;
-      }
-      with_act(p.act, [&](auto tag) {
-        constexpr int kAct = decltype(tag)::value;
-        v[0] = act_t<kAct>(g.x) * u.x;
-        v[1] = act_t<kAct>(g.y) * u.y;
-        v[2] = act_t<kAct>(g.z) * u.z;
-        v[3] = act_t<kAct>(g.w) * u.w;
-      });
-    } else {
-      uint2 res = make_uint2(0u, 0u);
-      if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + at);
-      float4 z = sum_ranks<kC>(sp);
-      if (p.bias != nullptr) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
-        z.x += bf16_lo(b.x);
-        z.y += bf16_hi(b.x);
-        z.z += bf16_lo(b.y);
-        z.w += bf16_hi(b.y);
-      }
-      if (p.save != nullptr) *reinterpret_cast<float4*>(p.save + at) = z;
-      with_act(p.act, [&](auto tag) {
-        constexpr int kAct = decltype(tag)::value;
-        v[0] = act_t<kAct>(z.x);
-        v[1] = act_t<kAct>(z.y);
-        v[2] = act_t<kAct>(z.z);
-        v[3] = act_t<kAct>(z.w);
-      });
-      if (p.residual != nullptr) {
-        v[0] += bf16_lo(res.x);
-        v[1] += bf16_hi(res.x);
-        v[2] += bf16_lo(res.y);
-        v[3] += bf16_hi(res.y);
-      }
-    }
-    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    const float4 z = sum_ranks<kC>(sp);
+    const float4 u = kGated ? sum_ranks<kC>(sp + p.rows * 4) : z;
+    write_outputs<kGated>(p, z, u, bias, res, t0 + t, n, aborted);
   }
 }
 
-template <bool kAmn, bool kGated>
+// Push: s_part holds [C][nt][len], the partials of this CTA's rows / C outputs
+// (gated: the gate sums, then the up sums). `bias` and `res` are the first
+// step's, loaded ahead of the barrier.
+template <bool kGated, int kC>
+__device__ __forceinline__ void finish_push(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
+                                            bool aborted, uint2 bias, uint2 res) {
+  const int own = p.rows / kC, len = kGated ? 2 * own : own, per = own / 4;
+  for (int i = threadIdx.x; i < nt * per; i += kThreads) {
+    const int t = i / per, r = (i - t * per) * 4;
+    const int n = n0 + rank * own + r;
+    if (n >= p.N) continue;
+    if (!kGated && i >= kThreads) load_addends(p, t0 + t, n, bias, res);
+    float4 g[kC], u[kC];
+#pragma unroll
+    for (int q = 0; q < kC; ++q) {
+      const float* s = s_part + (q * nt + t) * len + r;
+      g[q] = *reinterpret_cast<const float4*>(s);
+      if (kGated) u[q] = *reinterpret_cast<const float4*>(s + own);
+    }
+#pragma unroll
+    for (int q = 1; q < kC; ++q) {
+      g[0].x += g[q].x;
+      g[0].y += g[q].y;
+      g[0].z += g[q].z;
+      g[0].w += g[q].w;
+      if (kGated) {
+        u[0].x += u[q].x;
+        u[0].y += u[q].y;
+        u[0].z += u[q].z;
+        u[0].w += u[q].w;
+      }
+    }
+    write_outputs<kGated>(p, g[0], u[0], bias, res, t0 + t, n, aborted);
+  }
+}
+
+template <bool kAmn, bool kGated, bool kPush>
 __global__ void __launch_bounds__(kThreads)
     dense_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const SmallParams p) {
@@ -141,13 +197,15 @@ __global__ void __launch_bounds__(kThreads)
   const int kStages = p.stages;
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSmemBytes - kSlack - kBarrierBytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_status = reinterpret_cast<int*>(s_tmem + 2);
-  float* s_part = reinterpret_cast<float*>(smem);  // [nt][kLd], after the last MMA
+  volatile int* s_abort_any = reinterpret_cast<volatile int*>(s_tmem + 3);  // push: some CTA of the cluster gave up
+  // pull: [nt][kLd] in the ring, after the last MMA; push: the region above the ring
+  float* s_part = reinterpret_cast<float*>(kPush ? sB + kStages * kB : smem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int csize = static_cast<int>(cluster_nctarank());
@@ -167,6 +225,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     mbar_init(tfull, 1);
     *s_abort = 0;
+    *s_abort_any = 0;
     *s_status = 0;
     fence_mbarrier_init();
   }
@@ -182,6 +241,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
+  if (kPush) cluster_arrive();  // this CTA runs and has set its flags: its peers may store into it after their wait
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
 
@@ -249,46 +309,87 @@ __global__ void __launch_bounds__(kThreads)
         ph ^= 1;
       }
     }
-    if (one) umma_commit(tfull);
+    if (one) {
+      umma_commit(tfull);
+      // MMAs in flight end before the tensor memory is freed, also after a wait that gave up
+      int never = 0;
+      if (*s_abort) mbar_wait_bounded(tfull, 0, &never, s_status, 1000000ull);
+    }
+    __syncwarp();
   } else if (warp < 6) {
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
     const bool got = mbar_wait_bounded(tfull, 0, s_abort, s_status, p.timeout_ns) && *s_abort == 0;
-    if (__all_sync(0xffffffffu, got)) {
+    const bool ok = __all_sync(0xffffffffu, got);
+    if (kPush) cluster_wait();  // every CTA of the cluster runs
+    if (ok) {
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+      // push: where this thread's row goes
+      const int own = p.rows / csize, len = kGated ? 2 * own : own;
+      const int up = kGated && r >= p.rows ? 1 : 0, ru = r - up * p.rows;
+      const int owner = min(ru / own, csize - 1);  // rows past the unit go nowhere
+      const bool store = ru < p.rows;
+      const uint32_t dst = kPush ? cluster_map(smem_u32(s_part + rank * nt * len + up * own + (ru - owner * own)),
+                                               static_cast<uint32_t>(owner))
+                                 : 0u;
       for (int c = 0; c < p.n_pad; c += 16) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < nt) s_part[(c + i) * kLd + r] = __uint_as_float(v[i]);
+        for (int i = 0; i < 16; ++i) {
+          if (c + i >= nt) break;
+          if (!kPush)
+            s_part[(c + i) * kLd + r] = __uint_as_float(v[i]);
+          else if (store)
+            st_cluster_u32(dst + static_cast<uint32_t>((c + i) * len * 4), v[i]);
+        }
       }
+    } else if (kPush && lane < csize) {
+      st_cluster_u32(cluster_map(smem_u32(const_cast<int*>(s_abort_any)), static_cast<uint32_t>(lane)), 1u);
     }
   }
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // every CTA of the cluster has its partial in shared memory
+  uint2 bias = make_uint2(0u, 0u), res = bias;
+  if (kPush) {
+    __syncwarp();
+    if (warp < 2 || warp >= 6) cluster_wait();
+    if (!kGated) {  // the first step's addends are on their way during the barrier
+      const int own = p.rows / csize, per = own / 4;
+      const int t = threadIdx.x / per, r = (threadIdx.x - t * per) * 4;
+      if (t < nt) load_addends(p, t0 + t, n0 + rank * own + r, bias, res);
+    }
+  } else {
+    __syncthreads();
+  }
+  cluster_sync();  // every partial is where it is read
 
-  bool aborted = false;
-  for (int q = 0; q < csize; ++q)
-    aborted |= ld_cluster_s32(cluster_map(smem_u32(const_cast<int*>(s_abort)), static_cast<uint32_t>(q))) != 0;
+  bool aborted = kPush && *s_abort_any != 0;
+  if (!kPush)
+    for (int q = 0; q < csize; ++q)
+      aborted |= ld_cluster_s32(cluster_map(smem_u32(const_cast<int*>(s_abort)), static_cast<uint32_t>(q))) != 0;
+  auto finish = [&](auto c) {
+    constexpr int kC = decltype(c)::value;
+    if (kPush)
+      finish_push<kGated, kC>(p, s_part, n0, t0, nt, rank, aborted, bias, res);
+    else
+      finish_pull<kGated, kC>(p, s_part, n0, t0, nt, rank, aborted);
+  };
   switch (csize) {
     case 1:
-      finish<kGated, 1>(p, s_part, n0, t0, nt, rank, aborted);
+      finish(std::integral_constant<int, 1>{});
       break;
     case 2:
-      finish<kGated, 2>(p, s_part, n0, t0, nt, rank, aborted);
+      finish(std::integral_constant<int, 2>{});
       break;
     case 4:
-      finish<kGated, 4>(p, s_part, n0, t0, nt, rank, aborted);
+      finish(std::integral_constant<int, 4>{});
       break;
     default:
-      finish<kGated, 8>(p, s_part, n0, t0, nt, rank, aborted);
+      finish(std::integral_constant<int, 8>{});
   }
-  // no CTA leaves while another may still read its shared memory
-  cluster_sync();
+  if (!kPush) cluster_sync();  // no CTA leaves while another may still read its shared memory
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, p.n_alloc);
@@ -349,7 +450,8 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.n_pad = (p.tile_t + 15) / 16 * 16;
   p.n_alloc = 32;
   while (p.n_alloc < static_cast<uint32_t>(p.n_pad)) p.n_alloc <<= 1;
-  p.stages = std::min(kMaxStages, kRing / (kA + p.n_pad * kBK * 2));
+  const bool push = p.tile_t <= kPushTokens;
+  p.stages = ring_stages(p.tile_t, p.n_pad, push);
   p.act = g.act;
   p.stall = stall_gate_up_loads();
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
@@ -367,14 +469,14 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
       encode_tensor_map_2d(&tmX, bf16, 2, g.a, g.K, g.M, kBK, p.n_pad);
   if (!ok) return cudaErrorInvalidValue;
 
-  auto kernel = dense_small_kernel<kAmn, kGated>;
-  static unsigned long long done = 0;
-  cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
+  auto kernel = push ? dense_small_kernel<kAmn, kGated, true> : dense_small_kernel<kAmn, kGated, false>;
+  static unsigned long long done[2] = {0, 0};
+  cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done[push]);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = small_smem();
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
