@@ -28,13 +28,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, status, limit_ns));
 }
 
-// The two halves of cluster_sync, and a store into another CTA's shared memory.
+// The two halves of cluster_sync.
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+
+// Asynchronous store into the shared memory of a CTA of the cluster, its four
+// bytes counted on a barrier there.
+__device__ __forceinline__ void st_async_u32(uint32_t cluster_dst, uint32_t v, uint32_t cluster_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(cluster_dst),
+               "r"(v), "r"(cluster_bar)
+               : "memory");
 }
 
 // Shared-memory descriptor of an MN-major operand (its rows along K, 64

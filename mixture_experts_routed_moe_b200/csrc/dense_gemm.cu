@@ -583,10 +583,9 @@ Shape choose_shape(const DenseGemm* g, int n, int num_sms) {
     const int outn = gated ? cols / 2 : cols;
     long long tiles[2] = {0, 0};
     double each[2] = {0, 0};
-    for (int i = 0; i < n; ++i) {
-      tiles[i] = ((g[i].M + rows - 1ll) / rows) * ((g[i].N + outn - 1ll) / outn);
-      each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1.5;
-    }
+    for (int i = 0; i < n; ++i) tiles[i] = ((g[i].M + rows - 1ll) / rows) * ((g[i].N + outn - 1ll) / outn);
+    if (cols == 128 && tiles[0] + tiles[1] <= workers) per_step = 0.21;  // one round: nothing shared is full yet
+    for (int i = 0; i < n; ++i) each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1.5;
     // worker w has the tiles w, w + workers, ... of the list: the most loaded is
     // worker 0, or the one at which the first product's last round ends
     const long long all = (tiles[0] + tiles[1] + workers - 1) / workers;

@@ -5,21 +5,19 @@
 //   linear:  out[t, n] = bf16(act(sum_k W[n,k] X[t,k] + bias[n]) + residual[t, n])
 //   gated:   out[t, n] = bf16(act(sum_k W[n,k] X[t,k]) * sum_k W[N+n,k] X[t,k])
 //
-// for batches of up to a few hundred tokens, in even token tiles of at most 128,
+// for batches of up to a few hundred tokens, in even token tiles of at most 64,
 // with W read K-major, or MN-major (linear only: dx = dz W of the backward
 // pass, where W^T's rows are the outputs). A unit is up to 128 weight rows
 // (gated: as many gate rows as up rows); a cluster of C CTAs owns a unit, CTA r
 // taking the r-th of C ranges of K through a TMA ring into one TMEM
 // accumulator of 128 x n_pad. The CTAs share out the unit's outputs, each adding
 // the C partials of its part in rank order (one fixed order: deterministic, no
-// atomics) and applying the epilogue in fp32. How the partials travel:
-//   push  (token tiles of at most 64): each CTA stores its partial, row by row,
-//         straight from TMEM into the shared memory of the CTA that adds it, in
-//         a region of its own; one cluster barrier, and all reads are local
-//   pull  (wider tiles, whose region would take the ring's room): the partial
-//         goes to the CTA's own ring, which is free by then, and is read through
-//         distributed shared memory between two cluster barriers
-// From the last MMA to the end pull takes 3.1 us, push 1.7 (16 x 2048 -> 7168).
+// atomics) and applying the epilogue in fp32. A partial goes straight from TMEM
+// by asynchronous stores into the shared memory of the CTA that adds it, a
+// region of its own beside the ring, counted on a barrier there: nobody waits for a
+// remote load, for another CTA's ring or for a barrier of the cluster (from the
+// last MMA to the end, 16 x 2048 -> 7168: 3.1 us with partials read through
+// distributed shared memory between two cluster barriers, 1.9 so).
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 TMEM to shared memory, then all
 // eight reduce. Every wait is bounded; a cluster with a wait that gave up
@@ -36,9 +34,8 @@ namespace {
 constexpr int kBK = 64;
 constexpr int kThreads = 256;
 constexpr int kA = kTileM * kBK * 2;  // 16 KB of weights a stage
-constexpr int kLd = kTileM + 4;       // floats between two tokens' partial rows
 constexpr int kMaxStages = 12;
-constexpr int kTileTokens = 128;  // most tokens of a token tile
+constexpr int kTileTokens = 64;  // most tokens of a token tile
 
 struct SmallParams {
   int T, N, num_kb;
@@ -56,32 +53,15 @@ struct SmallParams {
 };
 
 // A CTA takes half an SM's shared memory (two CTAs of it, or one and the next
-// kernel's, which starts early): the ring, and for push the partials' region.
+// kernel's, which starts early): the ring and the partials' region.
 constexpr int kSmemBytes = 114688;
 constexpr int kSlack = 1024, kBarrierBytes = 512;
-constexpr int kPushTokens = 64;  // most tokens of a token tile that is pushed
-static_assert(kTileTokens * kLd * 4 <= kSmemBytes - kSlack - kBarrierBytes, "the partial rows reuse the ring");
-__host__ __device__ constexpr int region_bytes(int tile_t, bool push) { return push ? tile_t * kTileM * 4 : 0; }
-int ring_stages(int tile_t, int n_pad, bool push) {
-  const int ring = kSmemBytes - kSlack - kBarrierBytes - region_bytes(tile_t, push);
-  return std::min(kMaxStages, ring / (kA + n_pad * kBK * 2));
+constexpr int kRoom = kSmemBytes - kSlack - kBarrierBytes;
+__host__ __device__ constexpr int region_bytes(int tile_t) { return tile_t * kTileM * 4; }
+int ring_stages(int tile_t, int n_pad) {
+  return std::min(kMaxStages, (kRoom - region_bytes(tile_t)) / (kA + n_pad * kBK * 2));
 }
-
-// The C partials at one place, added in rank order; all loads are in flight together.
-template <int kC>
-__device__ __forceinline__ float4 sum_ranks(uint32_t addr) {
-  float4 v[kC];
-#pragma unroll
-  for (int q = 0; q < kC; ++q) v[q] = ld_cluster_f32x4(cluster_map(addr, static_cast<uint32_t>(q)));
-#pragma unroll
-  for (int q = 1; q < kC; ++q) {
-    v[0].x += v[q].x;
-    v[0].y += v[q].y;
-    v[0].z += v[q].z;
-    v[0].w += v[q].w;
-  }
-  return v[0];
-}
+static_assert(region_bytes(kTileTokens) * 2 <= kRoom, "a partial is put together in the ring");
 
 // Four consecutive outputs of one token, from their sums: bias, activation,
 // residual, the one rounding. `res` and `bias` are the four values' inputs.
@@ -132,37 +112,18 @@ __device__ __forceinline__ void load_addends(const SmallParams& p, int t, int n,
   if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + static_cast<size_t>(t) * p.N + n);
 }
 
-// Pull: this CTA's share of the unit's outputs, the partials read from their CTAs.
+// s_part holds [C][nt][len], the partials of this CTA's rows / C outputs (gated:
+// the gate sums, then the up sums). The addends of the first kAhead steps were
+// loaded while the partials travelled.
+constexpr int kAhead = 2;
 template <bool kGated, int kC>
-__device__ __forceinline__ void finish_pull(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
-                                            bool aborted) {
-  const int per = p.rows / 4;
-  const int items = nt * per;
-  for (int i = rank * items / kC + threadIdx.x; i < (rank + 1) * items / kC; i += kThreads) {
-    const int t = i / per, r = (i - t * per) * 4;
-    const int n = n0 + r;
-    if (n >= p.N) continue;  // N is a multiple of 8
-    uint2 bias, res;
-    if (!kGated) load_addends(p, t0 + t, n, bias, res);
-    const uint32_t sp = smem_u32(s_part + t * kLd + r);
-    const float4 z = sum_ranks<kC>(sp);
-    const float4 u = kGated ? sum_ranks<kC>(sp + p.rows * 4) : z;
-    write_outputs<kGated>(p, z, u, bias, res, t0 + t, n, aborted);
-  }
-}
-
-// Push: s_part holds [C][nt][len], the partials of this CTA's rows / C outputs
-// (gated: the gate sums, then the up sums). `bias` and `res` are the first
-// step's, loaded ahead of the barrier.
-template <bool kGated, int kC>
-__device__ __forceinline__ void finish_push(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
-                                            bool aborted, uint2 bias, uint2 res) {
+__device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
+                                       bool aborted, const uint2 (&bias)[kAhead], const uint2 (&res)[kAhead]) {
   const int own = p.rows / kC, len = kGated ? 2 * own : own, per = own / 4;
-  for (int i = threadIdx.x; i < nt * per; i += kThreads) {
+  auto step = [&](int i, uint2 bi, uint2 re) {
     const int t = i / per, r = (i - t * per) * 4;
     const int n = n0 + rank * own + r;
-    if (n >= p.N) continue;
-    if (!kGated && i >= kThreads) load_addends(p, t0 + t, n, bias, res);
+    if (n >= p.N) return;
     float4 g[kC], u[kC];
 #pragma unroll
     for (int q = 0; q < kC; ++q) {
@@ -183,11 +144,21 @@ __device__ __forceinline__ void finish_push(const SmallParams& p, const float* s
         u[0].w += u[q].w;
       }
     }
-    write_outputs<kGated>(p, g[0], u[0], bias, res, t0 + t, n, aborted);
+    write_outputs<kGated>(p, g[0], u[0], bi, re, t0 + t, n, aborted);
+  };
+  int i = threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k, i += kThreads)
+    if (i < nt * per) step(i, bias[k], res[k]);
+  for (; i < nt * per; i += kThreads) {
+    const int t = i / per;
+    uint2 bi, re;
+    load_addends(p, t0 + t, n0 + rank * own + (i - t * per) * 4, bi, re);
+    step(i, bi, re);
   }
 }
 
-template <bool kAmn, bool kGated, bool kPush>
+template <bool kAmn, bool kGated>
 __global__ void __launch_bounds__(kThreads)
     dense_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const SmallParams p) {
@@ -197,15 +168,14 @@ __global__ void __launch_bounds__(kThreads)
   const int kStages = p.stages;
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSmemBytes - kSlack - kBarrierBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRoom);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
+  uint64_t* arrived = tfull + 1;  // the partials of this CTA's outputs
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(arrived + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_status = reinterpret_cast<int*>(s_tmem + 2);
-  volatile int* s_abort_any = reinterpret_cast<volatile int*>(s_tmem + 3);  // push: some CTA of the cluster gave up
-  // pull: [nt][kLd] in the ring, after the last MMA; push: the region above the ring
-  float* s_part = reinterpret_cast<float*>(kPush ? sB + kStages * kB : smem);
+  float* s_part = reinterpret_cast<float*>(sB + kStages * kB);  // [C][nt][len], by source
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int csize = static_cast<int>(cluster_nctarank());
@@ -216,6 +186,8 @@ __global__ void __launch_bounds__(kThreads)
   const int t0 = (blockIdx.x / csize - unit * p.tiles) * p.tile_t;
   const int nt = min(p.tile_t, p.T - t0);
   const int kb0 = rank * p.num_kb / csize, kb1 = (rank + 1) * p.num_kb / csize;
+  // outputs that each CTA adds up, and their values a token
+  const int own = p.rows / csize, len = kGated ? 2 * own : own;
   // bytes a stage receives (an MN-major unit always has 128 rows)
   const uint32_t stage_bytes = static_cast<uint32_t>((kGated ? 2 : 1) * (kAmn ? 128 : p.rows) * 128 + kB);
   if (threadIdx.x == 0) {
@@ -224,10 +196,11 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
+    mbar_init(arrived, 1);
     *s_abort = 0;
-    *s_abort_any = 0;
     *s_status = 0;
     fence_mbarrier_init();
+    mbar_arrive_expect_tx(arrived, static_cast<uint32_t>(nt * (kGated ? 2 : 1) * p.rows * 4));
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmW);
@@ -241,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
-  if (kPush) cluster_arrive();  // this CTA runs and has set its flags: its peers may store into it after their wait
+  cluster_arrive();  // this CTA's barriers exist: its peers may copy into it after their wait
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
 
@@ -321,75 +294,60 @@ __global__ void __launch_bounds__(kThreads)
     const int r = quad * 32 + lane;
     const bool got = mbar_wait_bounded(tfull, 0, s_abort, s_status, p.timeout_ns) && *s_abort == 0;
     const bool ok = __all_sync(0xffffffffu, got);
-    if (kPush) cluster_wait();  // every CTA of the cluster runs
+    cluster_wait();  // every CTA of the cluster runs, with its barriers
     if (ok) {
       tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-      // push: where this thread's row goes
-      const int own = p.rows / csize, len = kGated ? 2 * own : own;
       const int up = kGated && r >= p.rows ? 1 : 0, ru = r - up * p.rows;
-      const int owner = min(ru / own, csize - 1);  // rows past the unit go nowhere
-      const bool store = ru < p.rows;
-      const uint32_t dst = kPush ? cluster_map(smem_u32(s_part + rank * nt * len + up * own + (ru - owner * own)),
-                                               static_cast<uint32_t>(owner))
-                                 : 0u;
+      const bool store = ru < p.rows;  // rows past the unit go nowhere
+      const int owner = store ? ru / own : 0;
+      const uint32_t dst = cluster_map(smem_u32(s_part + rank * nt * len + up * own + (ru - owner * own)),
+                                       static_cast<uint32_t>(owner));
+      const uint32_t bar = cluster_map(smem_u32(arrived), static_cast<uint32_t>(owner));
       for (int c = 0; c < p.n_pad; c += 16) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (c + i >= nt) break;
-          if (!kPush)
-            s_part[(c + i) * kLd + r] = __uint_as_float(v[i]);
-          else if (store)
-            st_cluster_u32(dst + static_cast<uint32_t>((c + i) * len * 4), v[i]);
-        }
+        for (int i = 0; i < 16; ++i)
+          if (store && c + i < nt) st_async_u32(dst + static_cast<uint32_t>((c + i) * len * 4), v[i], bar);
       }
-    } else if (kPush && lane < csize) {
-      st_cluster_u32(cluster_map(smem_u32(const_cast<int*>(s_abort_any)), static_cast<uint32_t>(lane)), 1u);
     }
   }
-  tc_fence_before();
-  uint2 bias = make_uint2(0u, 0u), res = bias;
-  if (kPush) {
+  if (warp < 2 || warp >= 6) {
     __syncwarp();
-    if (warp < 2 || warp >= 6) cluster_wait();
-    if (!kGated) {  // the first step's addends are on their way during the barrier
-      const int own = p.rows / csize, per = own / 4;
-      const int t = threadIdx.x / per, r = (threadIdx.x - t * per) * 4;
-      if (t < nt) load_addends(p, t0 + t, n0 + rank * own + r, bias, res);
-    }
-  } else {
-    __syncthreads();
+    cluster_wait();
   }
-  cluster_sync();  // every partial is where it is read
-
-  bool aborted = kPush && *s_abort_any != 0;
-  if (!kPush)
-    for (int q = 0; q < csize; ++q)
-      aborted |= ld_cluster_s32(cluster_map(smem_u32(const_cast<int*>(s_abort)), static_cast<uint32_t>(q))) != 0;
-  auto finish = [&](auto c) {
-    constexpr int kC = decltype(c)::value;
-    if (kPush)
-      finish_push<kGated, kC>(p, s_part, n0, t0, nt, rank, aborted, bias, res);
-    else
-      finish_pull<kGated, kC>(p, s_part, n0, t0, nt, rank, aborted);
+  uint2 bias[kAhead], res[kAhead];
+  if (!kGated) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = threadIdx.x + k * kThreads, per = own / 4, t = i / per;
+      bias[k] = res[k] = make_uint2(0u, 0u);
+      if (t < nt) load_addends(p, t0 + t, n0 + rank * own + (i - t * per) * 4, bias[k], res[k]);
+    }
+  }
+  // without regard to this CTA's own abort flag: copies of other CTAs may still be on their way here
+  int never = 0;
+  const bool aborted = !mbar_wait_bounded(arrived, 0, &never, s_status, p.timeout_ns);
+  tc_fence_before();
+  auto end = [&](auto c) {
+    finish<kGated, decltype(c)::value>(p, s_part, n0, t0, nt, rank, aborted, bias, res);
   };
   switch (csize) {
     case 1:
-      finish(std::integral_constant<int, 1>{});
+      end(std::integral_constant<int, 1>{});
       break;
     case 2:
-      finish(std::integral_constant<int, 2>{});
+      end(std::integral_constant<int, 2>{});
       break;
     case 4:
-      finish(std::integral_constant<int, 4>{});
+      end(std::integral_constant<int, 4>{});
       break;
     default:
-      finish(std::integral_constant<int, 8>{});
+      end(std::integral_constant<int, 8>{});
   }
-  if (!kPush) cluster_sync();  // no CTA leaves while another may still read its shared memory
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, p.n_alloc);
@@ -402,19 +360,19 @@ struct Plan {
   double us;  // estimated time; infinite where the CTAs would not be resident together
 };
 
-// The estimate, in us, from sweeps on B200 (weights of 2048 x 1408 to 14336 x
-// 4096, 16 to 1024 tokens): 5.5 for the launch, the first loads and the end; a
-// K step of a CTA at no less than 0.28, two CTAs of an SM sharing 150 KB/us;
-// the reduction with the partials it adds; 0.6 of the weights' time from HBM,
-// which the ring does not hide for so few steps. It is compared with the
-// tile kernel's, so it only has to be right to about a tenth.
+// The estimate, in us, from sweeps on B200 (weights of 2048 x 1408 to 7168 x
+// 2048, 1 to 768 tokens): 2.1 for the launch, the first loads and the end; a K
+// step of a CTA at no less than 0.20 and 110 KB/us, 180 for two CTAs of an SM; the
+// partials; half of the weights' time from HBM, which so few steps do not hide,
+// and some more where SMs with two CTAs run next to SMs with one. It is compared
+// with the tile kernel's, so it only has to be right to about a tenth.
 Plan plan_small(const DenseGemm& g, int num_sms) {
   const int num_kb = (g.K + kBK - 1) / kBK;
   const bool gated = g.order == kGatedNT;
   const double weights = 2.0 * g.N * g.K * (gated ? 2 : 1) / 6.0e6;
   Plan best{};
   best.us = std::numeric_limits<double>::infinity();
-  for (int cap = 32; cap <= kTileTokens; cap += 32) {
+  for (int cap = 16; cap <= kTileTokens; cap *= 2) {
     const long long tiles = (g.M + cap - 1ll) / cap;
     const int tile_t = static_cast<int>((g.M + tiles - 1) / tiles);
     const int n_pad = (tile_t + 15) / 16 * 16;
@@ -426,8 +384,10 @@ Plan plan_small(const DenseGemm& g, int num_sms) {
         // clusters that fit at two CTAs an SM
         if (ctas > num_sms * (c == 8 ? 1.78 : c == 4 ? 1.91 : 2.0)) continue;
         const double share = ctas > num_sms ? 2 : 1;
-        const double step = std::max(0.28, share * ((gated ? 2 : 1) * rows * 128 + n_pad * 128) / 150e3);
-        const double us = 5.5 + (num_kb + c - 1) / c * step + 0.3 * c * n_pad / 64 + (c == 8 ? 0.4 : 0.0) + 0.6 * weights;
+        const double bytes = (gated ? 2 : 1) * rows * 128 + n_pad * 128;
+        const double step = std::max(0.20, share > 1 ? bytes / 90e3 : bytes / 110e3);
+        const double us = 1.06 * (2.1 + (num_kb + c - 1) / c * step + 0.1 * c + 0.035 * tile_t + 0.5 * weights +
+                                  (share > 1 ? 0.3 + 0.1 * weights : 0.0));
         if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), us};
       }
     }
@@ -450,8 +410,7 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.n_pad = (p.tile_t + 15) / 16 * 16;
   p.n_alloc = 32;
   while (p.n_alloc < static_cast<uint32_t>(p.n_pad)) p.n_alloc <<= 1;
-  const bool push = p.tile_t <= kPushTokens;
-  p.stages = ring_stages(p.tile_t, p.n_pad, push);
+  p.stages = ring_stages(p.tile_t, p.n_pad);
   p.act = g.act;
   p.stall = stall_gate_up_loads();
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
@@ -469,9 +428,9 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
       encode_tensor_map_2d(&tmX, bf16, 2, g.a, g.K, g.M, kBK, p.n_pad);
   if (!ok) return cudaErrorInvalidValue;
 
-  auto kernel = push ? dense_small_kernel<kAmn, kGated, true> : dense_small_kernel<kAmn, kGated, false>;
-  static unsigned long long done[2] = {0, 0};
-  cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done[push]);
+  auto kernel = dense_small_kernel<kAmn, kGated>;
+  static unsigned long long done = 0;
+  cudaError_t err = ensure_max_smem(reinterpret_cast<const void*>(kernel), &done);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
