@@ -571,7 +571,7 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
 // 0.40-0.45 for 128 x 256 (a third more bytes through shared memory), but still
 // 0.26-0.29 at 128 columns: there the issuing warp's own path (wait, four MMAs,
 // commit: 0.20) and the bytes through shared memory, the same for half the
-// products, pace it. So the narrow tiles only pay where they save a wave. The sum has 2.6 us for the launch, the first loads
+// products, pace it. So the narrow tiles only pay where they save a wave. The sum has 3.4 us for the launch, the first loads
 // and the last tile's end, and a third of the weights' time from HBM.
 struct Shape {
   int best;
@@ -599,7 +599,7 @@ Shape choose_shape(const DenseGemm* g, int n, int num_sms) {
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[s.best]) s.best = i;
   const double bytes = 2.0 * g->K * (static_cast<double>(g->N) * (gated ? 2 : 1) + (n == 2 ? g->M : 0));
-  s.us = 2.6 + c[s.best] + 0.35 * bytes / 6.0e6;
+  s.us = 3.4 + c[s.best] + 0.35 * bytes / 6.0e6;
   return s;
 }
 

@@ -5,7 +5,7 @@
 //   linear:  out[t, n] = bf16(act(sum_k W[n,k] X[t,k] + bias[n]) + residual[t, n])
 //   gated:   out[t, n] = bf16(act(sum_k W[n,k] X[t,k]) * sum_k W[N+n,k] X[t,k])
 //
-// for batches of up to a few hundred tokens, in even token tiles of at most 64,
+// for batches of up to a few hundred tokens, in even token tiles of at most 128,
 // with W read K-major, or MN-major (linear only: dx = dz W of the backward
 // pass, where W^T's rows are the outputs). A unit is up to 128 weight rows
 // (gated: as many gate rows as up rows); a cluster of C CTAs owns a unit, CTA r
@@ -19,9 +19,8 @@
 // last MMA to the end, 16 x 2048 -> 7168: 3.1 us with partials read through
 // distributed shared memory between two cluster barriers, 1.9 so).
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2..5 TMEM to shared memory, then all
-// eight reduce. Every wait is bounded; a cluster with a wait that gave up
-// writes NaN.
+// Warps: 0 TMA producer, 1 MMA issuer; then all eight send and add. Every wait
+// is bounded; a cluster with a wait that gave up writes NaN.
 #include <algorithm>
 #include <limits>
 #include <type_traits>
@@ -35,7 +34,8 @@ constexpr int kBK = 64;
 constexpr int kThreads = 256;
 constexpr int kA = kTileM * kBK * 2;  // 16 KB of weights a stage
 constexpr int kMaxStages = 12;
-constexpr int kTileTokens = 64;  // most tokens of a token tile
+constexpr int kTileTokens = 128;  // most tokens of a token tile
+constexpr int kHalfTokens = 64;   // most tokens of a tile whose CTA takes half an SM
 
 struct SmallParams {
   int T, N, num_kb;
@@ -52,16 +52,16 @@ struct SmallParams {
   unsigned long long timeout_ns;
 };
 
-// A CTA takes half an SM's shared memory (two CTAs of it, or one and the next
-// kernel's, which starts early): the ring and the partials' region.
-constexpr int kSmemBytes = 114688;
+// Shared memory of a CTA, the ring and the partials' region: half an SM's (two
+// CTAs of it, or one and the next kernel's, which starts early), or all of it for
+// wide token tiles.
 constexpr int kSlack = 1024, kBarrierBytes = 512;
-constexpr int kRoom = kSmemBytes - kSlack - kBarrierBytes;
+__host__ __device__ constexpr int smem_bytes(int tile_t) { return tile_t <= kHalfTokens ? 114688 : 229376; }
+__host__ __device__ constexpr int room(int tile_t) { return smem_bytes(tile_t) - kSlack - kBarrierBytes; }
 __host__ __device__ constexpr int region_bytes(int tile_t) { return tile_t * kTileM * 4; }
 int ring_stages(int tile_t, int n_pad) {
-  return std::min(kMaxStages, (kRoom - region_bytes(tile_t)) / (kA + n_pad * kBK * 2));
+  return std::min(kMaxStages, (room(tile_t) - region_bytes(tile_t)) / (kA + n_pad * kBK * 2));
 }
-static_assert(region_bytes(kTileTokens) * 2 <= kRoom, "a partial is put together in the ring");
 
 // Four consecutive outputs of one token, from their sums: bias, activation,
 // residual, the one rounding. `res` and `bias` are the four values' inputs.
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads)
   const int kStages = p.stages;
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kA;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRoom);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + room(p.tile_t));
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* arrived = tfull + 1;  // the partials of this CTA's outputs
@@ -289,10 +289,15 @@ __global__ void __launch_bounds__(kThreads)
       if (*s_abort) mbar_wait_bounded(tfull, 0, &never, s_status, 1000000ull);
     }
     __syncwarp();
-  } else if (warp < 6) {
-    const int quad = warp & 3;
+  }
+  // All eight warps send the partial: two per TMEM lane quadrant, taking the
+  // blocks of 16 tokens in turn.
+  __syncwarp();
+  {
+    const int quad = warp & 3, first = warp >= 2 && warp < 6 ? 0 : 16;
     const int r = quad * 32 + lane;
-    const bool got = mbar_wait_bounded(tfull, 0, s_abort, s_status, p.timeout_ns) && *s_abort == 0;
+    const bool busy = first < p.n_pad;
+    const bool got = busy && mbar_wait_bounded(tfull, 0, s_abort, s_status, p.timeout_ns) && *s_abort == 0;
     const bool ok = __all_sync(0xffffffffu, got);
     cluster_wait();  // every CTA of the cluster runs, with its barriers
     if (ok) {
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(kThreads)
       const uint32_t dst = cluster_map(smem_u32(s_part + rank * nt * len + up * own + (ru - owner * own)),
                                        static_cast<uint32_t>(owner));
       const uint32_t bar = cluster_map(smem_u32(arrived), static_cast<uint32_t>(owner));
-      for (int c = 0; c < p.n_pad; c += 16) {
+      for (int c = first; c < p.n_pad; c += 32) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
         tmem_ld_wait();
@@ -313,10 +318,6 @@ __global__ void __launch_bounds__(kThreads)
           if (store && c + i < nt) st_async_u32(dst + static_cast<uint32_t>((c + i) * len * 4), v[i], bar);
       }
     }
-  }
-  if (warp < 2 || warp >= 6) {
-    __syncwarp();
-    cluster_wait();
   }
   uint2 bias[kAhead], res[kAhead];
   if (!kGated) {
@@ -381,13 +382,15 @@ Plan plan_small(const DenseGemm& g, int num_sms) {
       for (int rows = gated ? 64 : 128; rows >= 64; rows -= 64) {
         if (g.order == kLinearNN && rows != 128) continue;  // an MN-major unit is one box pair
         const long long ctas = ((g.N + rows - 1ll) / rows) * tiles * c;
-        // clusters that fit at two CTAs an SM
-        if (ctas > num_sms * (c == 8 ? 1.78 : c == 4 ? 1.91 : 2.0)) continue;
+        // clusters that fit, at two CTAs an SM or one
+        if (tile_t <= kHalfTokens ? ctas > num_sms * (c == 8 ? 1.78 : c == 4 ? 1.91 : 2.0)
+                                  : ctas > num_sms * (c == 8 ? 0.81 : c == 4 ? 0.89 : 1.0))
+          continue;
         const double share = ctas > num_sms ? 2 : 1;
         const double bytes = (gated ? 2 : 1) * rows * 128 + n_pad * 128;
         const double step = std::max(0.20, share > 1 ? bytes / 90e3 : bytes / 110e3);
         const double us = 1.06 * (2.1 + (num_kb + c - 1) / c * step + 0.1 * c + 0.035 * tile_t + 0.5 * weights +
-                                  (share > 1 ? 0.3 + 0.1 * weights : 0.0));
+                                  (share > 1 ? 0.7 + 0.2 * weights : 0.0));
         if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), us};
       }
     }
@@ -435,7 +438,7 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(p.tile_t));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
