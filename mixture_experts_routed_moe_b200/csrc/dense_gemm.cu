@@ -571,8 +571,9 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
 // 0.40-0.45 for 128 x 256 (a third more bytes through shared memory), but still
 // 0.26-0.29 at 128 columns: there the issuing warp's own path (wait, four MMAs,
 // commit: 0.20) and the bytes through shared memory, the same for half the
-// products, pace it. So the narrow tiles only pay where they save a wave. The sum has 3.4 us for the launch, the first loads
-// and the last tile's end, and a third of the weights' time from HBM.
+// products, pace it. So the narrow tiles only pay where they save a wave. The sum has 4.2 us for the launch, the first loads
+// and the last tile's end, and two thirds of the weights' time from HBM (off by
+// 8% over the sweep of the few-token form).
 struct Shape {
   int best;
   double us;
@@ -584,8 +585,8 @@ Shape choose_shape(const DenseGemm* g, int n, int num_sms) {
     long long tiles[2] = {0, 0};
     double each[2] = {0, 0};
     for (int i = 0; i < n; ++i) tiles[i] = ((g[i].M + rows - 1ll) / rows) * ((g[i].N + outn - 1ll) / outn);
-    if (cols == 128 && tiles[0] + tiles[1] <= workers) per_step = 0.21;  // one round: nothing shared is full yet
-    for (int i = 0; i < n; ++i) each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1.5;
+    if (tiles[0] + tiles[1] <= workers) per_step = cols == 128 ? 0.145 : 0.28;  // one round: nothing shared is full
+    for (int i = 0; i < n; ++i) each[i] = (g[i].K + kBK - 1ll) / kBK * per_step + 1.8;
     // worker w has the tiles w, w + workers, ... of the list: the most loaded is
     // worker 0, or the one at which the first product's last round ends
     const long long all = (tiles[0] + tiles[1] + workers - 1) / workers;
@@ -599,7 +600,7 @@ Shape choose_shape(const DenseGemm* g, int n, int num_sms) {
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[s.best]) s.best = i;
   const double bytes = 2.0 * g->K * (static_cast<double>(g->N) * (gated ? 2 : 1) + (n == 2 ? g->M : 0));
-  s.us = 3.4 + c[s.best] + 0.35 * bytes / 6.0e6;
+  s.us = 4.2 + c[s.best] + 0.67 * bytes / 6.0e6;
   return s;
 }
 

@@ -113,12 +113,12 @@ __device__ __forceinline__ void load_addends(const SmallParams& p, int t, int n,
 }
 
 // s_part holds [C][nt][len], the partials of this CTA's rows / C outputs (gated:
-// the gate sums, then the up sums). The addends of the first kAhead steps were
-// loaded while the partials travelled.
+// the gate sums, then the up sums). The addends are loaded kAhead steps ahead,
+// the first ones while the partials travel.
 constexpr int kAhead = 2;
 template <bool kGated, int kC>
 __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part, int n0, int t0, int nt, int rank,
-                                       bool aborted, const uint2 (&bias)[kAhead], const uint2 (&res)[kAhead]) {
+                                       bool aborted, uint2 (&bias)[kAhead], uint2 (&res)[kAhead]) {
   const int own = p.rows / kC, len = kGated ? 2 * own : own, per = own / 4;
   auto step = [&](int i, uint2 bi, uint2 re) {
     const int t = i / per, r = (i - t * per) * 4;
@@ -146,14 +146,17 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
     }
     write_outputs<kGated>(p, g[0], u[0], bi, re, t0 + t, n, aborted);
   };
-  int i = threadIdx.x;
+  for (int i = threadIdx.x; i < nt * per; i += kThreads) {
+    const uint2 bi = bias[0], re = res[0];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k, i += kThreads)
-    if (i < nt * per) step(i, bias[k], res[k]);
-  for (; i < nt * per; i += kThreads) {
-    const int t = i / per;
-    uint2 bi, re;
-    load_addends(p, t0 + t, n0 + rank * own + (i - t * per) * 4, bi, re);
+    for (int k = 1; k < kAhead; ++k) {
+      bias[k - 1] = bias[k];
+      res[k - 1] = res[k];
+    }
+    if (!kGated) {
+      const int j = i + kAhead * kThreads, t = j / per;
+      if (t < nt) load_addends(p, t0 + t, n0 + rank * own + (j - t * per) * 4, bias[kAhead - 1], res[kAhead - 1]);
+    }
     step(i, bi, re);
   }
 }
@@ -361,12 +364,13 @@ struct Plan {
   double us;  // estimated time; infinite where the CTAs would not be resident together
 };
 
-// The estimate, in us, from sweeps on B200 (weights of 2048 x 1408 to 7168 x
-// 2048, 1 to 768 tokens): 2.1 for the launch, the first loads and the end; a K
-// step of a CTA at no less than 0.20 and 110 KB/us, 180 for two CTAs of an SM; the
-// partials; half of the weights' time from HBM, which so few steps do not hide,
-// and some more where SMs with two CTAs run next to SMs with one. It is compared
-// with the tile kernel's, so it only has to be right to about a tenth.
+// The estimate, in us, fitted to sweeps on B200 (weights of 2048 x 1408 to 7168 x
+// 2048, 1 to 512 tokens, every shape): 2.1 for the launch, the first loads and
+// the end; a K step of a CTA at no less than 0.22, the ring's bytes in flight over
+// 0.94, and 266 KB/us (172 for two CTAs of an SM); the partials and the outputs;
+// a third of the weights' time from HBM, and some more where SMs with two CTAs
+// run next to SMs with one. Over the sweep it is off by 9% and the shapes it
+// picks are 1% from the best; the tile kernel's estimate is compared with it.
 Plan plan_small(const DenseGemm& g, int num_sms) {
   const int num_kb = (g.K + kBK - 1) / kBK;
   const bool gated = g.order == kGatedNT;
@@ -388,9 +392,9 @@ Plan plan_small(const DenseGemm& g, int num_sms) {
           continue;
         const double share = ctas > num_sms ? 2 : 1;
         const double bytes = (gated ? 2 : 1) * rows * 128 + n_pad * 128;
-        const double step = std::max(0.20, share > 1 ? bytes / 90e3 : bytes / 110e3);
-        const double us = 1.06 * (2.1 + (num_kb + c - 1) / c * step + 0.1 * c + 0.035 * tile_t + 0.5 * weights +
-                                  (share > 1 ? 0.7 + 0.2 * weights : 0.0));
+        const double step = std::max({0.22, 0.94 / ring_stages(tile_t, n_pad), bytes / (share > 1 ? 86e3 : 266e3)});
+        const double us = 2.1 + (num_kb + c - 1) / c * step + 0.13 * c + 0.022 * tile_t + 0.47 * tile_t * rows / c / 1024 +
+                          0.36 * weights + (share > 1 ? 1.1 + 0.16 * weights : 0.0);
         if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), us};
       }
     }
