@@ -22,6 +22,8 @@ from . import _FLOAT8, ACT, _check, _need, lib
 _BF16 = torch.bfloat16
 _F32 = torch.float32
 _LINEAR_ACT = dict(ACT, none=-1)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 @contextlib.contextmanager
@@ -45,18 +47,18 @@ def _operator(fn):
 
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            return fn(first, *args, **kw)  # refused inside, by name
-        if stream is None and first.get_device() == torch._C._cuda_getDevice():
-            return fn(first, *args, **kw)
+        try:
+            index = first.get_device()
+        except AttributeError:
+            index = -1
+        if index < 0 or (stream is None and index == _current_device()):
+            return fn(first, *args, **kw)  # (what is not on a CUDA device is refused inside, by name)
         with _on(first.device, stream):
             return fn(first, *args, **kw)
 
     return call
 
 
-def _current_stream(index):
-    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _tensor(t, name, dtype, shape, index):
@@ -75,6 +77,22 @@ def _first(t, name):
         _need(t, name, (_BF16,), 2, cuda=False)
         raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
     return t.shape, t.get_device()
+
+
+def _output(t, name, like, shape, index):
+    """(tensor, address) of the caller's bf16 output after its checks, or of a new
+    one of the type and device of the input `like`."""
+    if t is None:
+        t = torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+        return t, t.data_ptr()
+    return t, _tensor(t, name, _BF16, shape, index)
+
+
+def _rows(t, name):
+    """Rows of a weight matrix; its type, columns and device are checked by _tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _need(t, name, (_BF16,), 2, cuda=False)
+    return t.shape[0]
 
 
 def _workspace(ws, need, like):
@@ -119,12 +137,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
     s = x
     if residual is not None:
         r = _tensor(residual, "residual", _BF16, shape, dev)
-        s = torch.empty_like(x) if residual_out is None else residual_out
-        sp = _tensor(s, "residual_out", _BF16, shape, dev)
+        s, sp = _output(residual_out, "residual_out", x, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out was given without a residual")
-    y = torch.empty_like(x) if out is None else out
-    yp = _tensor(y, "out", _BF16, shape, dev)
+    y, yp = _output(out, "out", x, shape, dev)
     if quantize:
         codes = torch.empty_like(x, dtype=_FLOAT8)
         scales = x.new_empty((T, H // 128), dtype=_F32)
@@ -132,7 +148,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
     if rstd:
         rs = x.new_empty(T, dtype=_F32)
         rp = rs.data_ptr()
-    _check(lib().moe_rms_norm(x.data_ptr(), r, w, T, H, eps, yp, sp, cp, kp, rp, _current_stream(dev)), "moe_rms_norm")
+    _check(lib().moe_rms_norm(x.data_ptr(), r, w, T, H, eps, yp, sp, cp, kp, rp, _raw_stream(dev)), "moe_rms_norm")
     return RMSNormOutput(y, s, codes, scales, rs)
 
 
@@ -148,20 +164,18 @@ def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, wor
     w = _tensor(weight, "weight", _BF16, (H,), dev)
     r = _tensor(rstd, "rstd", _F32, (T,), dev)
     dr = None if dresidual is None else _tensor(dresidual, "dresidual", _BF16, shape, dev)
-    dx = torch.empty_like(dy) if dx is None else dx
-    dw = torch.empty_like(weight) if dw is None else dw
-    dxp, dwp = _tensor(dx, "dx", _BF16, shape, dev), _tensor(dw, "dw", _BF16, (H,), dev)
+    dx, dxp = _output(dx, "dx", dy, shape, dev)
+    dw, dwp = _output(dw, "dw", weight, (H,), dev)
     L = lib()
     ws = _workspace(workspace, L.moe_rms_norm_backward_workspace_size(T, H), dy)
     _check(L.moe_rms_norm_backward(dy.data_ptr(), sp, w, r, dr, T, H, dxp, dwp, ws.data_ptr(), ws.numel(),
-                                   _current_stream(dev)), "moe_rms_norm_backward")
+                                   _raw_stream(dev)), "moe_rms_norm_backward")
     return dx, dw
 
 
 def _gate_up(w_gate_up, H, dev):
     """(I, address) of the [2I,H] weight."""
-    _need(w_gate_up, "w_gate_up", (_BF16,), 2, cuda=False)
-    twoI = w_gate_up.shape[0]
+    twoI = _rows(w_gate_up, "w_gate_up")
     if twoI % 2 != 0:
         raise ValueError(f"w_gate_up: {twoI} rows, expected 2*I (gate rows, then up rows)")
     return twoI // 2, _tensor(w_gate_up, "w_gate_up", _BF16, (twoI, H), dev)
@@ -176,11 +190,10 @@ def gated_ffn(x, w_gate_up, act: str = "silu", save: bool = False, out=None):
     a = _act(act, ACT)
     (T, H), dev = _first(x, "x")
     I, w = _gate_up(w_gate_up, H, dev)
-    h = x.new_empty((T, I)) if out is None else out
-    hp = _tensor(h, "out", _BF16, (T, I), dev)
+    h, hp = _output(out, "out", x, (T, I), dev)
     gu = x.new_empty((T, 2 * I), dtype=_F32) if save else None
     _check(lib().moe_gated_ffn(x.data_ptr(), w, T, H, I, a, hp, gu.data_ptr() if save else None,
-                               _current_stream(dev)), "moe_gated_ffn")
+                               _raw_stream(dev)), "moe_gated_ffn")
     return (h, gu) if save else h
 
 
@@ -194,13 +207,12 @@ def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None
     I, w = _gate_up(w_gate_up, H, dev)
     d = _tensor(dh, "dh", _BF16, (T, I), dev)
     g = _tensor(gu, "gu", _F32, (T, 2 * I), dev)
-    dx = torch.empty_like(x) if dx is None else dx
-    dw = torch.empty_like(w_gate_up) if dw is None else dw
-    dxp, dwp = _tensor(dx, "dx", _BF16, shape, dev), _tensor(dw, "dw", _BF16, (2 * I, H), dev)
+    dx, dxp = _output(dx, "dx", x, shape, dev)
+    dw, dwp = _output(dw, "dw", w_gate_up, (2 * I, H), dev)
     L = lib()
     ws = _workspace(workspace, L.moe_gated_ffn_backward_workspace_size(T, I), x)
     _check(L.moe_gated_ffn_backward(d, x.data_ptr(), w, g, T, H, I, a, dxp, dwp, ws.data_ptr(), ws.numel(),
-                                    _current_stream(dev)), "moe_gated_ffn_backward")
+                                    _raw_stream(dev)), "moe_gated_ffn_backward")
     return dx, dw
 
 
@@ -212,16 +224,14 @@ def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False
     activation: the backward pass needs none). ``stream``: launch there."""
     a = _act(act, _LINEAR_ACT)
     (T, K), dev = _first(x, "x")
-    _need(w, "w", (_BF16,), 2, cuda=False)
-    N = w.shape[0]
+    N = _rows(w, "w")
     wp = _tensor(w, "w", _BF16, (N, K), dev)
     b = None if bias is None else _tensor(bias, "bias", _BF16, (N,), dev)
     r = None if residual is None else _tensor(residual, "residual", _BF16, (T, N), dev)
-    y = x.new_empty((T, N)) if out is None else out
-    yp = _tensor(y, "out", _BF16, (T, N), dev)
+    y, yp = _output(out, "out", x, (T, N), dev)
     z = x.new_empty((T, N), dtype=_F32) if save and act != "none" else None
     _check(lib().moe_linear(x.data_ptr(), wp, b, r, T, K, N, a, yp, None if z is None else z.data_ptr(),
-                            _current_stream(dev)), "moe_linear")
+                            _raw_stream(dev)), "moe_linear")
     return (y, z) if save else y
 
 
@@ -234,17 +244,15 @@ def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=
     a = _act(act, _LINEAR_ACT)
     shape, dev = _first(x, "x")
     T, K = shape
-    _need(w, "w", (_BF16,), 2, cuda=False)
-    N = w.shape[0]
+    N = _rows(w, "w")
     wp = _tensor(w, "w", _BF16, (N, K), dev)
     d = _tensor(dy, "dy", _BF16, (T, N), dev)
     zp = None if z is None else _tensor(z, "z", _F32, (T, N), dev)
-    dx = torch.empty_like(x) if dx is None else dx
-    dw = torch.empty_like(w) if dw is None else dw
-    dxp, dwp = _tensor(dx, "dx", _BF16, shape, dev), _tensor(dw, "dw", _BF16, (N, K), dev)
+    dx, dxp = _output(dx, "dx", x, shape, dev)
+    dw, dwp = _output(dw, "dw", w, (N, K), dev)
     db = w.new_empty(N) if bias else None
     L = lib()
     ws = _workspace(workspace, L.moe_linear_backward_workspace_size(T, N, a, int(bool(bias))), x)
     _check(L.moe_linear_backward(d, x.data_ptr(), wp, zp, T, K, N, a, dxp, dwp, None if db is None else db.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), _current_stream(dev)), "moe_linear_backward")
+                                 ws.data_ptr(), ws.numel(), _raw_stream(dev)), "moe_linear_backward")
     return dx, dw, db
