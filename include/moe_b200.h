@@ -366,10 +366,11 @@ moe_status moe_gated_ffn_backward(const void* dh, const void* x, const void* w_g
  *   x [T, K], w [N, K] bf16; bias [N] bf16 or NULL; residual [T, N] bf16 or NULL
  *   act   MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU or MOE_ACT_RELU
  *   y     [T, N] bf16 out; may be residual
- *   z     [T, N] fp32 out for the backward pass of an activation; or NULL
+ *   z     [T, N] bf16 out for the backward pass of an activation (it takes only
+ *         act'(z) of it); or NULL
  */
 moe_status moe_linear(const void* x, const void* w, const void* bias, const void* residual, int32_t T, int32_t K,
-                      int32_t N, int32_t act, void* y, float* z, void* stream);
+                      int32_t N, int32_t act, void* y, void* z, void* stream);
 
 /* Bytes of workspace moe_linear_backward needs (host-only; 0 for invalid
  * sizes); has_db: whether db is wanted. */
@@ -383,7 +384,7 @@ size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t act, int
  *   db = sum_t dz       [N] bf16 out, or NULL (summed from the fp32 dz)
  * The residual's gradient is dy. z may be NULL with MOE_ACT_NONE.
  */
-moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const float* z, int32_t T, int32_t K,
+moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const void* z, int32_t T, int32_t K,
                                int32_t N, int32_t act, void* dx, void* dw, void* db, void* workspace,
                                size_t workspace_bytes, void* stream);
 

@@ -156,7 +156,7 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate_up, int32_t T, int32_
   g.b = w_gate_up;
   g.out = h;
   g.act = act;
-  g.save0 = gu;
+  g.save = gu;
   return done(run(g, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -190,14 +190,14 @@ moe_status moe_gated_ffn_backward(const void* dh, const void* x, const void* w_g
 }
 
 moe_status moe_linear(const void* x, const void* w, const void* bias, const void* residual, int32_t T, int32_t K,
-                      int32_t N, int32_t act, void* y, float* z, void* stream) {
+                      int32_t N, int32_t act, void* y, void* z, void* stream) {
   if (T < 0 || !dim_ok(K) || !dim_ok(N) || !act_ok(act)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (x == nullptr || w == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(y, 16) ||
       !aligned(z, 16))
     return MOE_ERR_INVALID_ARG;
-  const Span sy{y, bf16_bytes(T, N)}, sz{z, f32_bytes(T, N)}, sr{residual, bf16_bytes(T, N)};
+  const Span sy{y, bf16_bytes(T, N)}, sz{z, bf16_bytes(T, N)}, sr{residual, bf16_bytes(T, N)};
   if (!disjoint({sy, sz}, {{x, bf16_bytes(T, K)}, {w, bf16_bytes(N, K)}, {bias, bf16_bytes(1, N)}}) ||
       !disjoint({sz}, {sr}) || !same_or_disjoint(sy, sr))
     return MOE_ERR_INVALID_ARG;
@@ -214,7 +214,7 @@ moe_status moe_linear(const void* x, const void* w, const void* bias, const void
   g.act = act;
   g.bias = bias;
   g.residual = residual;
-  g.save0 = z;
+  g.save = z;
   return done(run(g, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -224,7 +224,7 @@ size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t act, int
          (has_db ? round256(f32_bytes(linear_grad_rows(T, N), N)) : 0);
 }
 
-moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const float* z, int32_t T, int32_t K,
+moe_status moe_linear_backward(const void* dy, const void* x, const void* w, const void* z, int32_t T, int32_t K,
                                int32_t N, int32_t act, void* dx, void* dw, void* db, void* workspace,
                                size_t workspace_bytes, void* stream) {
   const size_t need = moe_linear_backward_workspace_size(T, N, act, db != nullptr);
@@ -244,7 +244,7 @@ moe_status moe_linear_backward(const void* dy, const void* x, const void* w, con
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   if (!disjoint({{dx, bf16_bytes(T, K)}, {dw, bf16_bytes(N, K)}, {db, bf16_bytes(1, N)}, {workspace, need}},
                 {{dy, bf16_bytes(T, N)}, {x, bf16_bytes(T, K)}, {w, bf16_bytes(N, K)},
-                 {act != MOE_ACT_NONE ? z : nullptr, f32_bytes(T, N)}}))
+                 {act != MOE_ACT_NONE ? z : nullptr, bf16_bytes(T, N)}}))
     return MOE_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;

@@ -3,8 +3,10 @@
 //
 //   linear:  out[m, n] = bf16(act(sum_k A[m,k] B[n,k] + bias[n]) + residual[m, n])
 //   gated:   out[m, n] = bf16(act(sum_k A[m,k] B[n,k]) * sum_k A[m,k] B[N+n,k])
-// optionally keeping the fp32 pre-activations (linear z[m,n]; gated g and u)
-// for the backward pass. The products of the backward pass run in one launch:
+// optionally keeping the pre-activations for the backward pass: the gated g and u
+// in fp32 (they multiply the gradients), the linear z in bf16 (only act'(z) is
+// taken of it: |z act''(z)| < 0.5 keeps the rounding's part of the slope below
+// 2^-9, less than the rounding of dz that follows, for half the bytes). The products of the backward pass run in one launch:
 //   dx = d W       A = d K-major, B = W MN-major
 //   dW = d^T x     both MN-major
 // Nothing is transposed in memory, and the tiles of both products share the
@@ -59,7 +61,7 @@ struct GemmParams {
   unsigned long long timeout_ns;
 };
 
-// Tensor maps of the products' operands and outputs; save: fp32 z, or g and u.
+// Tensor maps of the products' operands and outputs; save: z, or g and u.
 struct GemmMaps {
   CUtensorMap a[2], b[2], y[2], save[2];
 };
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (p.save) st.store_f32(&maps.save[0], v, x, y0, N, rows);
+          if (p.save) st.store_bf16(&maps.save[0], v, x, y0, rows && x < N);
           if (p.act != kActNone) {
             with_act(p.act, [&](auto tag) {
 #pragma unroll
@@ -517,19 +519,21 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
     maps.y[1] = maps.y[0];
   }
   p.act = g->act;
-  p.save = g->save0 != nullptr;
+  p.save = g->save != nullptr;
   p.stall = stall_gate_up_loads();
   p.bias = static_cast<const __nv_bfloat16*>(g->bias);
   p.residual = static_cast<const __nv_bfloat16*>(g->residual);
   p.timeout_ns = wait_limit_ns();
   maps.save[0] = maps.save[1] = maps.y[0];
   if (p.save) {
-    const uint64_t ld = kGated ? 2 * static_cast<uint64_t>(g->N) : g->N;
-    for (int i = 0; i < (kGated ? 2 : 1); ++i)
-      if (!encode_tensor_map_2d_ld(&maps.save[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
-                                   g->save0 + static_cast<size_t>(i) * g->N, g->N, g->M, ld, 16, 32,
-                                   CU_TENSOR_MAP_SWIZZLE_64B))
-        return cudaErrorInvalidValue;
+    for (int i = 0; i < (kGated ? 2 : 1); ++i) {
+      const bool encoded =
+          kGated ? encode_tensor_map_2d_ld(&maps.save[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+                                           static_cast<float*>(g->save) + static_cast<size_t>(i) * g->N, g->N, g->M,
+                                           2 * static_cast<uint64_t>(g->N), 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)
+                 : encode_tensor_map_2d(&maps.save[i], bf16, 2, g->save, g->N, g->M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+      if (!encoded) return cudaErrorInvalidValue;
+    }
   }
 
   auto kernel = dense_gemm_kernel<kPair, kBN, kMode>;

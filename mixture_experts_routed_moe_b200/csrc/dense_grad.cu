@@ -1,5 +1,6 @@
 // Elementwise halves of the dense operators' backward passes: the gradients
-// at the pre-activations, from the fp32 pre-activations the forward kept.
+// at the pre-activations, from the pre-activations the forward kept (g and u in
+// fp32, z in bf16).
 //
 //   gated:  dg = dh u act'(g),  du = dh act(g)        -> bf16 [T, 2I]
 //   linear: dz = dy act'(z)                           -> bf16 [T, N]
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict
 // written, the fp32 column sums of the range added over the warps in order and
 // left in partial[y].
 template <int kAct>
-__global__ void __launch_bounds__(256, 4) linear_grad_kernel(const float* __restrict__ z,
+__global__ void __launch_bounds__(256, 4) linear_grad_kernel(const __nv_bfloat16* __restrict__ z,
                                                           const __nv_bfloat16* __restrict__ dy,
                                                           __nv_bfloat16* __restrict__ dz, float* __restrict__ partial,
                                                           long long T, int N) {
@@ -70,20 +71,19 @@ __global__ void __launch_bounds__(256, 4) linear_grad_kernel(const float* __rest
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < N) {
     for (long long t = t0 + warp; t < t1; t += 8 * kRows) {
-      uint2 d[kRows];
-      float4 zz[kRows];
+      uint2 d[kRows], zz[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const size_t at = static_cast<size_t>(t + 8 * k) * N + c;
         d[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint2*>(dy + at) : make_uint2(0u, 0u);
         if (kAct != kActNone)
-          zz[k] = t + 8 * k < t1 ? *reinterpret_cast<const float4*>(z + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+          zz[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint2*>(z + at) : make_uint2(0u, 0u);
       }
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         float v[4] = {bf16_lo(d[k].x), bf16_hi(d[k].x), bf16_lo(d[k].y), bf16_hi(d[k].y)};
         if (kAct != kActNone) {
-          const float zk[4] = {zz[k].x, zz[k].y, zz[k].z, zz[k].w};
+          const float zk[4] = {bf16_lo(zz[k].x), bf16_hi(zz[k].x), bf16_lo(zz[k].y), bf16_hi(zz[k].y)};
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float f, s;
@@ -131,12 +131,13 @@ int linear_grad_rows(int T, int N) {
   return std::max(1, std::min((T + 63) / 64, std::max(1, 592 / cols)));
 }
 
-cudaError_t launch_linear_grad(const float* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
+cudaError_t launch_linear_grad(const void* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
                                int act, cudaStream_t st) {
   const int rows = linear_grad_rows(T, N);
   const dim3 grid(static_cast<unsigned>((N + kGradCols - 1) / kGradCols), static_cast<unsigned>(rows));
   const cudaError_t err = with_act(act, [&](auto tag) {
-    return launch_pdl(linear_grad_kernel<decltype(tag)::value>, grid, dim3(256), 0, st, z,
+    return launch_pdl(linear_grad_kernel<decltype(tag)::value>, grid, dim3(256), 0, st,
+                      static_cast<const __nv_bfloat16*>(z),
                       static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dz),
                       db != nullptr ? partial : static_cast<float*>(nullptr), static_cast<long long>(T), N);
   });

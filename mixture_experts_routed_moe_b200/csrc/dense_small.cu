@@ -48,7 +48,7 @@ struct SmallParams {
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
   __nv_bfloat16* out;
-  float* save;  // linear z [T, N]; gated [T, 2N]
+  void* save;  // linear: bf16 z [T, N]; gated: fp32 [T, 2N]; or null
   unsigned long long timeout_ns;
 };
 
@@ -77,9 +77,14 @@ __device__ __forceinline__ void write_outputs(const SmallParams& p, float4 z, fl
     z.w += bf16_hi(bias.y);
   }
   if (p.save != nullptr) {
-    float* s = p.save + (kGated ? 2 * static_cast<size_t>(t) * p.N + n : at);
-    *reinterpret_cast<float4*>(s) = z;
-    if (kGated) *reinterpret_cast<float4*>(s + p.N) = u;
+    if (kGated) {
+      float* s = static_cast<float*>(p.save) + 2 * static_cast<size_t>(t) * p.N + n;
+      *reinterpret_cast<float4*>(s) = z;
+      *reinterpret_cast<float4*>(s + p.N) = u;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.save) + at) =
+          make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
+    }
   }
   with_act(p.act, [&](auto tag) {
     constexpr int kAct = decltype(tag)::value;
@@ -423,7 +428,7 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
   p.residual = static_cast<const __nv_bfloat16*>(g.residual);
   p.out = static_cast<__nv_bfloat16*>(g.out);
-  p.save = g.save0;
+  p.save = g.save;
   p.timeout_ns = wait_limit_ns();
 
   const auto bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

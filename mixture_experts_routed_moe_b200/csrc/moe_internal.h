@@ -126,7 +126,7 @@ struct DenseGemm {
   int act = kActNone;
   const void* bias = nullptr;      // [N] bf16
   const void* residual = nullptr;  // [M, N] bf16, may be out
-  float* save0 = nullptr;          // fp32 pre-activations: linear [M, N], gated [M, 2N]
+  void* save = nullptr;            // pre-activations: linear bf16 [M, N], gated fp32 [M, 2N]
 };
 
 cudaError_t launch_dense_gemm(const DenseGemm& g, int num_sms, cudaStream_t st);
@@ -144,7 +144,7 @@ double dense_small_us(const DenseGemm& g, int num_sms);
 cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T, int I, int act, int num_sms,
                               cudaStream_t st);
 int linear_grad_rows(int T, int N);
-cudaError_t launch_linear_grad(const float* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
+cudaError_t launch_linear_grad(const void* z, const void* dy, void* dz, float* partial, void* db, int T, int N,
                                int act, cudaStream_t st);
 
 // out[c] = bf16(sum over rows of partial[r, c]), fixed order.

@@ -219,7 +219,7 @@ def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None
 @_operator
 def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False, out=None):
     """moe_linear: y = act(x W^T + bias) + residual, w [N,K], rounded once. ``out``
-    may be residual. Returns y bf16 [T,N]; with save, (y, z) with the fp32
+    may be residual. Returns y bf16 [T,N]; with save, (y, z) with the bf16
     pre-activation [T,N] that ``linear_backward`` takes (None without an
     activation: the backward pass needs none). ``stream``: launch there."""
     a = _act(act, _LINEAR_ACT)
@@ -229,7 +229,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False
     b = None if bias is None else _tensor(bias, "bias", _BF16, (N,), dev)
     r = None if residual is None else _tensor(residual, "residual", _BF16, (T, N), dev)
     y, yp = _output(out, "out", x, (T, N), dev)
-    z = x.new_empty((T, N), dtype=_F32) if save and act != "none" else None
+    z = x.new_empty((T, N)) if save and act != "none" else None
     _check(lib().moe_linear(x.data_ptr(), wp, b, r, T, K, N, a, yp, None if z is None else z.data_ptr(),
                             _raw_stream(dev)), "moe_linear")
     return (y, z) if save else y
@@ -247,7 +247,7 @@ def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=
     N = _rows(w, "w")
     wp = _tensor(w, "w", _BF16, (N, K), dev)
     d = _tensor(dy, "dy", _BF16, (T, N), dev)
-    zp = None if z is None else _tensor(z, "z", _F32, (T, N), dev)
+    zp = None if z is None else _tensor(z, "z", _BF16, (T, N), dev)
     dx, dxp = _output(dx, "dx", x, shape, dev)
     dw, dwp = _output(dw, "dw", w, (N, K), dev)
     db = w.new_empty(N) if bias else None

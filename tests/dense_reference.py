@@ -116,7 +116,8 @@ def linear_grads(dy, x, w, bias, name):
         eb = e
     else:
         edge = (z.abs() <= ez).double() if name == "relu" else 0.0
-        eb = dy.abs() * (CURVE[name] * ez + edge + FP32)
+        kept = ez + HALF * (z.abs() + ez)  # the forward keeps z in bf16
+        eb = dy.abs() * (CURVE[name] * kept + edge + FP32)
         e = eb + HALF * (dz.abs() + eb)
     dx, dw, ex, ew = _grads(dz, e, x, w)
     db = dz.sum(0)

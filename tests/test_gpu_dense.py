@@ -187,7 +187,7 @@ def test_linear(T, K, N, name, bias, residual):
     if name == "none":
         assert z is None
     else:
-        R.check(z, zr, ez + 2.0 ** -24 * zr.abs(), "z")
+        R.check(z, zr, ez + R.HALF * (zr.abs() + ez), "z")
     assert torch.equal(moe.linear(x, w, bias=b, act=name, residual=r), y)
     if residual:
         r2 = r.clone()
