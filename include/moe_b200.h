@@ -285,8 +285,8 @@ moe_status moe_forward_noalloc_status(void* stream);
  * `stream`, allocate nothing and are deterministic. T = 0 is valid (outputs
  * with no token rows are untouched, weight gradients are set to zero).
  *
- * Requirements, else MOE_ERR_INVALID_ARG: sizes other than T positive
- * multiples of 8 and at most 2^20 (H of the norm at most 65536); bf16 and fp32
+ * Requirements, else MOE_ERR_INVALID_ARG: T at most 2^30, the other sizes
+ * positive multiples of 8 and at most 2^20 (H of the norm at most 65536); bf16 and fp32
  * matrices 16-byte aligned, rstd and scales 4-byte aligned, workspaces 256-byte
  * aligned; no output overlaps an input or another output, except where an
  * entry point allows the two to be the same buffer. MOE_ERR_WORKSPACE for a
@@ -303,6 +303,7 @@ moe_status moe_forward_noalloc_status(void* stream);
  *   x, residual   [T, H] bf16; residual may be NULL
  *   weight        [H] bf16
  *   eps           > 0, finite
+ *   (the sum of squares is fp32: rows whose squares overflow it give zeros)
  *   y             [T, H] bf16 out, or NULL when only codes are wanted
  *   residual_out  [T, H] bf16 out: s, or NULL
  *   codes, scales e4m3 [T, H] and fp32 [T, H/128] out, or both NULL: the fp32 y

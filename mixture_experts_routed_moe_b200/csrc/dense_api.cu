@@ -13,8 +13,10 @@ namespace {
 
 constexpr int32_t kMaxDim = 1 << 20;
 constexpr int32_t kMaxNormH = 65536;
+constexpr int32_t kMaxT = 1 << 30;  // row numbers of a last tile stay below 2^31
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool rows_ok(int32_t T) { return T >= 0 && T <= kMaxT; }
 bool dim_ok(int32_t v) { return v >= 8 && v <= kMaxDim && v % 8 == 0; }
 bool gate_ok(int32_t act) { return act == MOE_ACT_SILU || act == MOE_ACT_GELU || act == MOE_ACT_RELU; }
 bool act_ok(int32_t act) { return act == MOE_ACT_NONE || gate_ok(act); }
@@ -89,7 +91,7 @@ extern "C" {
 
 moe_status moe_rms_norm(const void* x, const void* residual, const void* weight, int32_t T, int32_t H, float eps,
                         void* y, void* residual_out, uint8_t* codes, float* scales, float* rstd, void* stream) {
-  if (T < 0 || !dim_ok(H) || H > kMaxNormH || !std::isfinite(eps) || !(eps > 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(T) || !dim_ok(H) || H > kMaxNormH || !std::isfinite(eps) || !(eps > 0.0f)) return MOE_ERR_INVALID_ARG;
   if ((codes == nullptr) != (scales == nullptr) || (codes != nullptr && H % 128 != 0)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (x == nullptr || weight == nullptr || (y == nullptr && codes == nullptr)) return MOE_ERR_INVALID_ARG;
@@ -110,7 +112,7 @@ moe_status moe_rms_norm(const void* x, const void* residual, const void* weight,
 }
 
 size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H) {
-  if (T < 0 || !dim_ok(H) || H > kMaxNormH) return 0;
+  if (!rows_ok(T) || !dim_ok(H) || H > kMaxNormH) return 0;
   return round256(f32_bytes(std::max(1, rms_norm_backward_blocks(T, H)), H));
 }
 
@@ -128,17 +130,18 @@ moe_status moe_rms_norm_backward(const void* dy, const void* s, const void* weig
     return MOE_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   const size_t n = bf16_bytes(T, H), row = bf16_bytes(1, H);
-  const Span sdy{dy, n}, ss{s, n}, sw{weight, row}, sr{rstd, f32_bytes(T, 1)}, sd{dresidual, n}, sx{dx, n}, sdw{dw, row},
-      sws{workspace, need};
+  const Span sdy{dy, n}, ss{s, n}, sw{weight, row}, sr{rstd, f32_bytes(T, 1)}, sd{dresidual, n};
+  const Span sx{dx, n}, sdw{dw, row}, sws{workspace, need};
   if (!disjoint({sx, sdw, sws}, {ss, sw, sr}) || !disjoint({sdw, sws}, {sdy, sd}) || !same_or_disjoint(sx, sdy) ||
       !same_or_disjoint(sx, sd))
     return MOE_ERR_INVALID_ARG;
-  return done(launch_rms_norm_backward(dy, s, weight, rstd, dresidual, T, H, dx, dw, static_cast<float*>(workspace), st));
+  return done(launch_rms_norm_backward(dy, s, weight, rstd, dresidual, T, H, dx, dw, static_cast<float*>(workspace),
+                                       st));
 }
 
 moe_status moe_gated_ffn(const void* x, const void* w_gate_up, int32_t T, int32_t H, int32_t I, int32_t act, void* h,
                          float* gu, void* stream) {
-  if (T < 0 || !dim_ok(H) || !dim_ok(I) || !gate_ok(act)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(T) || !dim_ok(H) || !dim_ok(I) || !gate_ok(act)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (x == nullptr || w_gate_up == nullptr || h == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w_gate_up, 16) || !aligned(h, 16) || !aligned(gu, 16)) return MOE_ERR_INVALID_ARG;
@@ -161,7 +164,7 @@ moe_status moe_gated_ffn(const void* x, const void* w_gate_up, int32_t T, int32_
 }
 
 size_t moe_gated_ffn_backward_workspace_size(int32_t T, int32_t I) {
-  if (T < 0 || !dim_ok(I)) return 0;
+  if (!rows_ok(T) || !dim_ok(I)) return 0;
   return round256(std::max<size_t>(256, bf16_bytes(T, 2ll * I)));
 }
 
@@ -191,7 +194,7 @@ moe_status moe_gated_ffn_backward(const void* dh, const void* x, const void* w_g
 
 moe_status moe_linear(const void* x, const void* w, const void* bias, const void* residual, int32_t T, int32_t K,
                       int32_t N, int32_t act, void* y, void* z, void* stream) {
-  if (T < 0 || !dim_ok(K) || !dim_ok(N) || !act_ok(act)) return MOE_ERR_INVALID_ARG;
+  if (!rows_ok(T) || !dim_ok(K) || !dim_ok(N) || !act_ok(act)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (x == nullptr || w == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(y, 16) ||
@@ -219,7 +222,7 @@ moe_status moe_linear(const void* x, const void* w, const void* bias, const void
 }
 
 size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t act, int32_t has_db) {
-  if (T < 0 || !dim_ok(N) || !act_ok(act)) return 0;
+  if (!rows_ok(T) || !dim_ok(N) || !act_ok(act)) return 0;
   return 256 + (act != MOE_ACT_NONE ? round256(bf16_bytes(T, N)) : 0) +
          (has_db ? round256(f32_bytes(linear_grad_rows(T, N), N)) : 0);
 }

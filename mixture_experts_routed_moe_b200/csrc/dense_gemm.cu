@@ -6,7 +6,9 @@
 // optionally keeping the pre-activations for the backward pass: the gated g and u
 // in fp32 (they multiply the gradients), the linear z in bf16 (only act'(z) is
 // taken of it: |z act''(z)| < 0.5 keeps the rounding's part of the slope below
-// 2^-9, less than the rounding of dz that follows, for half the bytes). The products of the backward pass run in one launch:
+// 2^-9, less than the rounding of dz that follows, for half the bytes).
+//
+// The products of the backward pass run in one launch:
 //   dx = d W       A = d K-major, B = W MN-major
 //   dW = d^T x     both MN-major
 // Nothing is transposed in memory, and the tiles of both products share the
@@ -54,7 +56,7 @@ struct Product {
 
 struct GemmParams {
   Product prod[2];  // the second only in backward mode
-  int first_tiles, full, tiles;  // tiles of the first product; whole tiles of both, list length with the half ones
+  int first_tiles, full, tiles;  // tiles of the first product; whole tiles of both; with the half ones
   int act, save, stall;
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
@@ -239,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (one) {
-            if (leader) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(TL::kCtas * TL::kA + c.nb * kBK * 2));
+            if (leader)
+              mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(TL::kCtas * TL::kA + c.nb * kBK * 2));
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
               if (kPair)
                 tma_load_2d_pair(dst, map, leader_addr(&full[stage]), x, y);
@@ -370,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = y0 + lane < M;
       // the residual of the first columns is on its way while the tile's MMAs run
       const __nv_bfloat16* res =
-          kMode == kModeLinear && p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * N : nullptr;
+          kMode == kModeLinear && p.residual != nullptr && mine ? p.residual + static_cast<size_t>(y0 + lane) * N
+                                                                : nullptr;
       uint4 rv[4];
       auto load_res = [&](int x) {
 #pragma unroll
@@ -575,9 +579,10 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
 // 0.40-0.45 for 128 x 256 (a third more bytes through shared memory), but still
 // 0.26-0.29 at 128 columns: there the issuing warp's own path (wait, four MMAs,
 // commit: 0.20) and the bytes through shared memory, the same for half the
-// products, pace it. So the narrow tiles only pay where they save a wave. The sum has 4.2 us for the launch, the first loads
-// and the last tile's end, and two thirds of the weights' time from HBM (off by
-// 8% over the sweep of the few-token form).
+// products, pace it. So the narrow tiles only pay where they save a wave. The
+// sum has 4.2 us for the launch, the first loads and the last tile's end, and two
+// thirds of the weights' time from HBM (off by 8% over the sweep of the few-token
+// form).
 struct Shape {
   int best;
   double us;

@@ -398,8 +398,9 @@ Plan plan_small(const DenseGemm& g, int num_sms) {
         const double share = ctas > num_sms ? 2 : 1;
         const double bytes = (gated ? 2 : 1) * rows * 128 + n_pad * 128;
         const double step = std::max({0.22, 0.94 / ring_stages(tile_t, n_pad), bytes / (share > 1 ? 86e3 : 266e3)});
-        const double us = 2.1 + (num_kb + c - 1) / c * step + 0.13 * c + 0.022 * tile_t + 0.47 * tile_t * rows / c / 1024 +
-                          0.36 * weights + (share > 1 ? 1.1 + 0.16 * weights : 0.0);
+        const double us = 2.1 + (num_kb + c - 1) / c * step + 0.13 * c + 0.022 * tile_t +
+                          0.47 * tile_t * rows / c / 1024 + 0.36 * weights +
+                          (share > 1 ? 1.1 + 0.16 * weights : 0.0);
         if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), us};
       }
     }

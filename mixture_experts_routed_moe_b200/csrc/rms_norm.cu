@@ -159,8 +159,15 @@ __device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, 
 // i + tpr, ...; the 16 vectors of a 128-column group lie in one half-warp. The
 // grid is a few blocks an SM; each row group walks over its rows with the next
 // row's loads in flight while it reduces and stores the current one.
+//
+// Measured on B200 (CUDA graph, inputs from HBM): 8192 x 2048 with a residual
+// 22.9 us = 5.86 TB/s, 0.89 of the measured copy bandwidth; 4096 x 8192 43.4 us =
+// 6.18 TB/s; 4096 x 7168 with codes 47.4 us = 5.59 TB/s; one row 1.7 us. Bulk copies
+// of rows through a ring in shared memory (3 to 6 stages) measured 24 to 30 us
+// on the first, one block a row without the walk 26.
 template <int kVec, int kMaxThreads, bool kRes, bool kCodes>
-__global__ void __launch_bounds__(kMaxThreads, !kRes && kVec == 1 && kMaxThreads == 512 ? 3 : 1) rms_norm_kernel(const NormParams p, int tpr) {
+__global__ void __launch_bounds__(kMaxThreads, !kRes && kVec == 1 && kMaxThreads == 512 ? 3 : 1)
+    rms_norm_kernel(const NormParams p, int tpr) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
   __shared__ float s_red[2][32 * kVec];
@@ -225,7 +232,8 @@ struct NormBwdParams {
 // r over its rows in registers. The block adds its groups' sums in order and
 // writes one partial row, which column_sum_kernel adds over the blocks. With
 // kPrefetch the next row's loads are in flight during the reduction and the
-// stores of the current one; without (rows so wide that the sums of dw take the
+// stores of the current one (4099 x 4096 with a residual's gradient: 26.7 us, the
+// column sums included, = 5.03 TB/s); without (rows so wide that the sums of dw take the
 // registers) the second pass over the row reads it again, from the caches.
 template <int kVec, int kMaxThreads, bool kPrefetch>
 __global__ void __launch_bounds__(kMaxThreads) rms_norm_backward_kernel(const NormBwdParams p, int tpr) {

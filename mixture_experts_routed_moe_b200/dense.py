@@ -45,16 +45,19 @@ def _operator(fn):
     them. The common case (current device, current stream) is passed straight on:
     small calls are bound by the host."""
 
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         try:
             index = first.get_device()
         except AttributeError:
             index = -1
         if index < 0 or (stream is None and index == _current_device()):
-            return fn(first, *args, **kw)  # (what is not on a CUDA device is refused inside, by name)
+            return fn(*args, **kw)  # (what is not on a CUDA device is refused inside, by name)
         with _on(first.device, stream):
-            return fn(first, *args, **kw)
+            return fn(*args, **kw)
 
     return call
 

@@ -35,7 +35,7 @@ def norm_args():
 
 
 @pytest.mark.parametrize("bad", [
-    dict(T=-1), dict(H=0), dict(H=100), dict(H=65544), dict(eps=0.0), dict(eps=-1.0), dict(eps=math.inf),
+    dict(T=-1), dict(T=(1 << 30) + 1), dict(H=0), dict(H=100), dict(H=65544), dict(eps=0.0), dict(eps=-1.0), dict(eps=math.inf),
     dict(eps=math.nan), dict(x=None), dict(weight=None), dict(codes=None), dict(scales=None), dict(H=264),
     dict(y=None, codes=None, scales=None), dict(x=at(0) + 8), dict(residual=at(1) + 2), dict(weight=at(2) + 8),
     dict(y=at(3) + 4), dict(residual_out=at(4) + 8), dict(codes=at(5) + 1), dict(scales=at(6) + 2),

@@ -24,14 +24,18 @@ def normal(seed, *shape, std=1.0, mean=0.0):
 def block_of(wl, seed, Is=192, shared=True):
     W = G.make_weights(wl, seed, device="cuda")
     layer = moe.MoELayer(W["w_gate_up"], W["w_down"], wl.k, W.get("sw_gate_up"), W.get("sw_down"))
-    extra = dict(shared_gate_up=normal(3, 2 * Is, wl.H, std=wl.H ** -0.5), shared_down=normal(4, wl.H, Is, std=Is ** -0.5)) if shared else {}
+    extra = {}
+    if shared:
+        extra = dict(shared_gate_up=normal(3, 2 * Is, wl.H, std=wl.H ** -0.5),
+                     shared_down=normal(4, wl.H, Is, std=Is ** -0.5))
     return moe.MoEBlock(layer, normal(1, wl.H, std=0.2, mean=1.0), G.make_router_weights(wl, seed, device="cuda"),
                         **extra), W
 
 
 BLOCKS = [G.Workload("block", 64, 256, 256, 8, 2), G.Workload("block", 1, 256, 128, 16, 4),
           G.Workload("block", 301, 512, 256, 16, 4), G.Workload("block", 5, 256, 256, 8, 2, wdtype="e4m3"),
-          G.Workload("block", 300, 512, 256, 8, 2, wdtype="e4m3"), G.Workload("block", 40, 256, 256, 8, 2, wdtype="e2m1")]
+          G.Workload("block", 300, 512, 256, 8, 2, wdtype="e4m3"),
+          G.Workload("block", 40, 256, 256, 8, 2, wdtype="e2m1")]
 
 
 @pytest.mark.parametrize("wl", BLOCKS, ids=lambda w: f"{w.wdtype}-{w.T}")
@@ -180,6 +184,13 @@ def test_streams_and_graphs(name):
         torch.cuda.synchronize()
         for _, out in graphs:
             assert _same(out, want)
+
+
+def test_arguments_by_name():
+    x, w, wg, wl = normal(1, 3, 64), normal(2, 64), normal(3, 32, 64), normal(4, 24, 64)
+    assert torch.equal(moe.rms_norm(x=x, weight=w).y, moe.rms_norm(x, w).y)
+    assert torch.equal(moe.gated_ffn(w_gate_up=wg, x=x, act="gelu"), moe.gated_ffn(x, wg, act="gelu"))
+    assert torch.equal(moe.linear(w=wl, x=x, stream=torch.cuda.current_stream()), moe.linear(x, wl))
 
 
 def test_stream_of_another_kind_is_refused():

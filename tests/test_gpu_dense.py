@@ -25,7 +25,8 @@ NORM_SIZES = [(1, 2048), (1, 8), (3, 64), (129, 128), (5, 1024), (7, 1032), (33,
 
 
 # batches whose rows outnumber the blocks, at widths with 1, 2 and 4 vectors a thread
-NORM_MANY = [(1500, 1032), (2500, 2048), (1000, 4096), (1203, 4104), (700, 7168), (801, 8192), (611, 8200), (500, 16384)]
+NORM_MANY = [(1500, 1032), (2500, 2048), (1000, 4096), (1203, 4104), (700, 7168), (801, 8192), (611, 8200),
+             (500, 16384)]
 
 
 @pytest.mark.parametrize("T,H", NORM_SIZES + NORM_MANY)
