@@ -275,3 +275,22 @@ def test_a_wait_that_gives_up_marks_the_outputs(T):
     for t in (h, y, dx, dw):
         assert torch.isnan(t).all()
     assert torch.equal(moe.gated_ffn(x, wg), want) and torch.equal(moe.linear(want, wd), y_want)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose element offsets pass 2^31 (and byte offsets 2^32): the last rows
+    equal the same rows computed alone."""
+    T, H, I = 270_000, 64, 8192  # h: 2.2e9 elements
+    x, wg = normal(1, T, H), normal(2, 2 * I, H, std=0.1)
+    h = moe.gated_ffn(x, wg)
+    want, bound = R.gated(x[-5:], wg, "silu")[::2]
+    R.check(h[-5:], want, bound, "h")
+    wd, b = normal(3, H, I, std=0.01), normal(4, H)
+    y = moe.linear(h, wd, bias=b, residual=x)
+    want, _, bound, _ = R.linear(h[-5:], wd, b, "none", x[-5:])
+    R.check(y[-5:], want, bound, "y")
+    w = normal(5, I, std=0.1, mean=1.0)
+    n = moe.rms_norm(h, w, residual=h, residual_out=h, quantize=True)
+    few = moe.rms_norm(h[-5:].contiguous(), w, quantize=True)  # (h holds the sums now)
+    assert torch.equal(n.y[-5:], few.y) and torch.equal(n.scales[-5:], few.scales)
+    assert torch.equal(n.codes[-5:].view(torch.uint8), few.codes.view(torch.uint8))
