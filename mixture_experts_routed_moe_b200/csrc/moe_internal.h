@@ -107,7 +107,7 @@ cudaError_t launch_fused_decode(const moe_shape* s, const Plan& p, const void* x
 // ---- dense operators around the routed experts ----
 
 constexpr int kActNone = MOE_ACT_NONE;
-constexpr int kNormBackwardBlocks = 296;  // row classes of the norm's weight gradient (two per SM of a B200)
+constexpr int kNormBackwardSms = 148;   // SMs that the norm's backward pass and its workspace are sized for
 
 // Operand orders of a dense GEMM with out [M, N].
 enum DenseOrder {
