@@ -211,3 +211,53 @@ def test_linear_backward(T, K, N, name, bias):
         R.check(db, rb, eb, "db")
     else:
         assert db is None
+
+
+# ---- one token --------------------------------------------------------------
+
+# one, two, four and eight warps to a row, a K below one load a lane, ends inside a batch of
+# loads, outputs that end inside a block, and the size from which K takes the tensor cores
+ONE = [(8, 8), (16, 4104), (264, 72), (1032, 8), (1000, 2040), (2056, 1032), (2048, 8192), (4096, 8), (4104, 24),
+       (8200, 520), (7168, 2048), (16392, 40), (24584, 2056)]
+
+
+@pytest.mark.parametrize("K,N", ONE)
+@pytest.mark.parametrize("name,bias,residual,save", [("none", False, False, False), ("none", True, True, False),
+                                                     ("gelu", True, True, True), ("relu", False, True, True)])
+def test_linear_one_token(K, N, name, bias, residual, save):
+    x, w = normal(K, 1, K), normal(K + N, N, K, std=K ** -0.5)
+    b = normal(N, N, std=0.5) if bias else None
+    r = normal(N + 1, 1, N) if residual else None
+    around = torch.full((3, N), 7.0, device="cuda", dtype=BF)
+    out = moe.linear(x, w, bias=b, act=name, residual=r, out=around[1:2], save=save)
+    z = out[1] if save else None
+    ref, zr, bound, ez = R.linear(x, w, b, name, r)
+    R.check(around[1:2], ref, bound, "y")
+    assert bool((around[0] == 7).all()) and bool((around[2] == 7).all())
+    if save:
+        R.check(z, zr, ez + R.HALF * (zr.abs() + ez), "z")
+
+
+@pytest.mark.parametrize("K,N", ONE)
+@pytest.mark.parametrize("name,save", [("silu", False), ("gelu", True)])
+def test_gated_one_token(K, N, name, save):
+    x, w = normal(K, 1, K), normal(K + N, 2 * N, K, std=K ** -0.5)
+    around = torch.full((3, N), 7.0, device="cuda", dtype=BF)
+    got = moe.gated_ffn(x, w, act=name, out=around[1:2], save=save)
+    ref, z, bound, ez = R.gated(x, w, name)
+    R.check(around[1:2], ref, bound, "h")
+    assert bool((around[0] == 7).all()) and bool((around[2] == 7).all())
+    if save:
+        R.check(got[1], z, ez, "gu")
+
+
+def test_one_token_keeps_a_bad_row_to_its_output():
+    x, w = normal(1, 1, 1000), normal(2, 520, 1000, std=0.03)
+    y = moe.linear(x, w)
+    w[77, 999] = float("nan")
+    w[130, 0] = float("inf")
+    bad = moe.linear(x, w)
+    rest = torch.ones(520, dtype=torch.bool, device="cuda")
+    rest[77] = rest[130] = False
+    assert bool(bad[0, 77].isnan()) and bool(bad[0, 130].isinf())
+    assert torch.equal(bad[:, rest], y[:, rest])
