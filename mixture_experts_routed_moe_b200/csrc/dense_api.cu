@@ -52,7 +52,7 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 moe_status done(cudaError_t err) { return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 cudaError_t run(const DenseGemm& g, int sms, cudaStream_t st) {
-  if (dense_vec_supported(g)) return launch_dense_vec(g, sms, st);
+  if (dense_vec_supported(g, sms)) return launch_dense_vec(g, sms, st);
   return dense_small_us(g, sms) < dense_gemm_us(g, sms) ? launch_dense_small(g, sms, st)
                                                         : launch_dense_gemm(g, sms, st);
 }

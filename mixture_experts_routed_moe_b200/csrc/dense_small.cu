@@ -5,9 +5,10 @@
 //   linear:  out[t, n] = bf16(act(sum_k W[n,k] X[t,k] + bias[n]) + residual[t, n])
 //   gated:   out[t, n] = bf16(act(sum_k W[n,k] X[t,k]) * sum_k W[N+n,k] X[t,k])
 //
-// for batches of two to a few hundred tokens (one token: only the largest weights), in even token tiles of at most 128,
-// with W read K-major, or MN-major (linear only: dx = dz W of the backward
-// pass, where W^T's rows are the outputs). A unit is up to 128 weight rows
+// for batches of up to a few hundred tokens (the smallest go through registers instead,
+// but for dx and the largest weights), in even token tiles of at most 128, with W read
+// K-major, or MN-major (linear only: dx = dz W of the backward pass, where W^T's rows
+// are the outputs). A unit is up to 128 weight rows
 // (gated: as many gate rows as up rows); a cluster of C CTAs owns a unit, CTA r
 // taking the r-th of C ranges of K through a TMA ring into one TMEM
 // accumulator of 128 x n_pad. The CTAs share out the unit's outputs, each adding

@@ -135,8 +135,8 @@ cudaError_t launch_dense_gemm_backward(const DenseGemm& dx, const DenseGemm& dw,
 // The form for few tokens (M), weights streamed with K split over clusters.
 cudaError_t launch_dense_small(const DenseGemm& g, int num_sms, cudaStream_t st);
 
-// The form for a single token, K-major weights.
-bool dense_vec_supported(const DenseGemm& g);
+// The form for up to 24 tokens, K-major weights, where it is the faster one.
+bool dense_vec_supported(const DenseGemm& g, int num_sms);
 cudaError_t launch_dense_vec(const DenseGemm& g, int num_sms, cudaStream_t st);
 
 // Estimated times in us, by which the entry points choose between the forms

@@ -255,7 +255,7 @@ def test_nan_and_infinite_rows_stay_in_their_rows(T):
     assert torch.isnan(h[1]).all() and torch.isnan(y[1]).all()
 
 
-@pytest.mark.parametrize("T", [4, 700])
+@pytest.mark.parametrize("T", [40, 700])
 def test_a_wait_that_gives_up_marks_the_outputs(T):
     """With loads withheld and a 20 ms limit the GEMMs' waits run out: the call
     returns, every output is NaN, and the next call gives the right bits."""

@@ -215,8 +215,8 @@ def test_linear_backward(T, K, N, name, bias):
 
 # ---- one token --------------------------------------------------------------
 
-# one, two, four and eight warps to a row, a K below one load a lane, ends inside a batch of
-# loads, outputs that end inside a block, and the size from which K takes the tensor cores
+# four, eight and sixteen warps to a row, a K below one load a lane, ends inside a lane's, a
+# warp's and a batch's loads, outputs that end inside a unit, and large weights
 ONE = [(8, 8), (16, 4104), (264, 72), (1032, 8), (1000, 2040), (2056, 1032), (2048, 8192), (4096, 8), (4104, 24),
        (8200, 520), (7168, 2048), (16392, 40), (24584, 2056)]
 
@@ -261,3 +261,57 @@ def test_one_token_keeps_a_bad_row_to_its_output():
     rest[77] = rest[130] = False
     assert bool(bad[0, 77].isnan()) and bool(bad[0, 130].isinf())
     assert torch.equal(bad[:, rest], y[:, rest])
+
+
+# ---- a few tokens -----------------------------------------------------------
+
+# the group of eight tokens that ends, K and N as above, weights on either side of the rules
+# between the forms; 16-byte rows and bases as well as 32-byte ones
+FEW = [(2, 8, 8), (5, 40, 24), (7, 1408, 2048), (8, 2056, 1032), (9, 16, 4104), (12, 4096, 136), (15, 7168, 264),
+       (16, 2048, 9480), (16, 5120, 5000), (17, 1032, 520), (23, 8192, 72), (24, 2048, 4736), (25, 2048, 1408)]
+
+
+@pytest.mark.parametrize("T,K,N", FEW)
+@pytest.mark.parametrize("shift", [0, 8])
+@pytest.mark.parametrize("name,bias,residual,save", [("none", False, False, False), ("silu", True, True, True)])
+def test_linear_few_tokens(T, K, N, shift, name, bias, residual, save):
+    x, w = normal(T, T * K + shift)[shift:].view(T, K), normal(K + N, N * K + shift, std=K ** -0.5)[shift:].view(N, K)
+    b = normal(N, N, std=0.5) if bias else None
+    r = normal(N + 1, T, N) if residual else None
+    around = torch.full((T + 2, N), 7.0, device="cuda", dtype=BF)
+    out = moe.linear(x, w, bias=b, act=name, residual=r, out=around[1:T + 1], save=save)
+    ref, zr, bound, ez = R.linear(x, w, b, name, r)
+    R.check(around[1:T + 1], ref, bound, "y")
+    assert bool((around[0] == 7).all()) and bool((around[T + 1] == 7).all())
+    if save:
+        R.check(out[1], zr, ez + R.HALF * (zr.abs() + ez), "z")
+    if residual:
+        assert torch.equal(moe.linear(x, w, bias=b, act=name, residual=r, out=r), around[1:T + 1])
+
+
+@pytest.mark.parametrize("T,K,N", FEW)
+@pytest.mark.parametrize("shift", [0, 8])
+@pytest.mark.parametrize("name,save", [("silu", False), ("relu", True)])
+def test_gated_few_tokens(T, K, N, shift, name, save):
+    x = normal(T, T * K + shift)[shift:].view(T, K)
+    w = normal(K + N, 2 * N * K + shift, std=K ** -0.5)[shift:].view(2 * N, K)
+    around = torch.full((T + 2, N), 7.0, device="cuda", dtype=BF)
+    got = moe.gated_ffn(x, w, act=name, out=around[1:T + 1], save=save)
+    ref, z, bound, ez = R.gated(x, w, name)
+    R.check(around[1:T + 1], ref, bound, "h")
+    assert bool((around[0] == 7).all()) and bool((around[T + 1] == 7).all())
+    if save:
+        R.check(got[1], z, ez, "gu")
+
+
+@pytest.mark.parametrize("T", [3, 11, 20])
+def test_few_tokens_keep_bad_rows_apart(T):
+    x, w = normal(1, T, 1000), normal(2, 520, 1000, std=0.03)
+    y = moe.linear(x, w)
+    w[77, 999] = float("nan")
+    x[2, 0] = float("inf")
+    bad = moe.linear(x, w)
+    assert bool(bad[:, 77].isnan().all()) and not bool(bad[2].isfinite().any())
+    rows = torch.arange(T, device="cuda") != 2
+    cols = torch.arange(520, device="cuda") != 77
+    assert torch.equal(bad[rows][:, cols], y[rows][:, cols])
