@@ -12,7 +12,6 @@ every call can be captured in a CUDA graph after one eager call.
 from __future__ import annotations
 
 import contextlib
-import functools
 import typing
 
 import torch
@@ -38,30 +37,11 @@ def _on(device, stream):
             yield
 
 
-def _operator(fn):
-    """An entry point whose first argument fixes the device: it runs with that
-    device current and the caller's stream, if given, as the current stream, so
-    that outputs and workspaces allocated inside belong to the stream that uses
-    them. The common case (current device, current stream) is passed straight on:
-    small calls are bound by the host."""
-
-    name = fn.__code__.co_varnames[0]
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        first = args[0] if args else kw.get(name)
-        try:
-            index = first.get_device()
-        except AttributeError:
-            index = -1
-        if index < 0 or (stream is None and index == _current_device()):
-            return fn(*args, **kw)  # (what is not on a CUDA device is refused inside, by name)
-        with _on(first.device, stream):
-            return fn(*args, **kw)
-
-    return call
-
-
+# Every entry point passes a call for another device than the current one, or with a
+# stream, once through itself with that device and stream current (_on): outputs and
+# workspaces allocated inside then belong to the stream that uses them.
+def _elsewhere(index, stream):
+    return stream is not None or index != _current_device()
 
 
 def _tensor(t, name, dtype, shape, index):
@@ -86,7 +66,7 @@ def _output(t, name, like, shape, index):
     """(tensor, address) of the caller's bf16 output after its checks, or of a new
     one of the type and device of the input `like`."""
     if t is None:
-        t = torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+        t = torch.empty_like(like) if like.shape == shape else like.new_empty(*shape)
         return t, t.data_ptr()
     return t, _tensor(t, name, _BF16, shape, index)
 
@@ -126,14 +106,16 @@ class RMSNormOutput(typing.NamedTuple):
     rstd: torch.Tensor | None = None
 
 
-@_operator
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False, rstd: bool = False, out=None,
-             residual_out=None) -> RMSNormOutput:
+             residual_out=None, stream=None) -> RMSNormOutput:
     """moe_rms_norm: s = x + residual (rounded to bf16, the residual stream),
     y = s * (mean(s^2) + eps)^(-1/2) * weight. ``out`` and ``residual_out`` may be
     x or residual for an in-place step. ``quantize`` adds y in the form of the
     FP8 experts' activations (H a multiple of 128). ``stream``: launch there."""
     shape, dev = _first(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(x.device, stream):
+            return rms_norm(x, weight, residual, eps, quantize, rstd, out, residual_out)
     T, H = shape
     w = _tensor(weight, "weight", _BF16, (H,), dev)
     r = sp = cp = kp = rp = codes = scales = rs = None
@@ -146,7 +128,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
     y, yp = _output(out, "out", x, shape, dev)
     if quantize:
         codes = torch.empty_like(x, dtype=_FLOAT8)
-        scales = x.new_empty((T, H // 128), dtype=_F32)
+        scales = x.new_empty(T, H // 128, dtype=_F32)
         cp, kp = codes.data_ptr(), scales.data_ptr()
     if rstd:
         rs = x.new_empty(T, dtype=_F32)
@@ -155,13 +137,15 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
     return RMSNormOutput(y, s, codes, scales, rs)
 
 
-@_operator
-def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, workspace=None):
+def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, workspace=None, stream=None):
     """moe_rms_norm_backward: (dx bf16 [T,H], dw bf16 [H]) from the gradient dy at
     y and dresidual at the residual stream; s, weight and rstd are the
     forward's (``RMSNormOutput.residual`` and ``.rstd``). dx is the gradient of x
     and of the residual alike. ``stream``: launch there."""
     shape, dev = _first(dy, "dy")
+    if _elsewhere(dev, stream):
+        with _on(dy.device, stream):
+            return rms_norm_backward(dy, s, weight, rstd, dresidual, dx, dw, workspace)
     T, H = shape
     sp = _tensor(s, "s", _BF16, shape, dev)
     w = _tensor(weight, "weight", _BF16, (H,), dev)
@@ -184,28 +168,32 @@ def _gate_up(w_gate_up, H, dev):
     return twoI // 2, _tensor(w_gate_up, "w_gate_up", _BF16, (twoI, H), dev)
 
 
-@_operator
-def gated_ffn(x, w_gate_up, act: str = "silu", save: bool = False, out=None):
+def gated_ffn(x, w_gate_up, act: str = "silu", save: bool = False, out=None, stream=None):
     """moe_gated_ffn: h = act(x Wg^T) * (x Wu^T) in one kernel, w_gate_up [2I,H]
     the gate rows and then the up rows (one expert's layout). Returns h bf16
     [T,I]; with save, (h, gu) with the fp32 pre-activations [T,2I] that
     ``gated_ffn_backward`` takes. ``stream``: launch there."""
     a = _act(act, ACT)
     (T, H), dev = _first(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(x.device, stream):
+            return gated_ffn(x, w_gate_up, act, save, out)
     I, w = _gate_up(w_gate_up, H, dev)
     h, hp = _output(out, "out", x, (T, I), dev)
-    gu = x.new_empty((T, 2 * I), dtype=_F32) if save else None
+    gu = x.new_empty(T, 2 * I, dtype=_F32) if save else None
     _check(lib().moe_gated_ffn(x.data_ptr(), w, T, H, I, a, hp, gu.data_ptr() if save else None,
                                _raw_stream(dev)), "moe_gated_ffn")
     return (h, gu) if save else h
 
 
-@_operator
-def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None, workspace=None):
+def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None, workspace=None, stream=None):
     """moe_gated_ffn_backward: (dx bf16 [T,H], dw bf16 [2I,H]) from dh [T,I], with
     x, w_gate_up and the gu that the forward kept. ``stream``: launch there."""
     a = _act(act, ACT)
     shape, dev = _first(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(x.device, stream):
+            return gated_ffn_backward(dh, x, w_gate_up, gu, act, dx, dw, workspace)
     T, H = shape
     I, w = _gate_up(w_gate_up, H, dev)
     d = _tensor(dh, "dh", _BF16, (T, I), dev)
@@ -219,33 +207,39 @@ def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None
     return dx, dw
 
 
-@_operator
-def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False, out=None):
+def linear(x, w, bias=None, act: str = "none", residual=None, save: bool = False, out=None,
+           stream=None):
     """moe_linear: y = act(x W^T + bias) + residual, w [N,K], rounded once. ``out``
     may be residual. Returns y bf16 [T,N]; with save, (y, z) with the bf16
     pre-activation [T,N] that ``linear_backward`` takes (None without an
     activation: the backward pass needs none). ``stream``: launch there."""
     a = _act(act, _LINEAR_ACT)
     (T, K), dev = _first(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(x.device, stream):
+            return linear(x, w, bias, act, residual, save, out)
     N = _rows(w, "w")
     wp = _tensor(w, "w", _BF16, (N, K), dev)
     b = None if bias is None else _tensor(bias, "bias", _BF16, (N,), dev)
     r = None if residual is None else _tensor(residual, "residual", _BF16, (T, N), dev)
     y, yp = _output(out, "out", x, (T, N), dev)
-    z = x.new_empty((T, N)) if save and act != "none" else None
+    z = x.new_empty(T, N) if save and act != "none" else None
     _check(lib().moe_linear(x.data_ptr(), wp, b, r, T, K, N, a, yp, None if z is None else z.data_ptr(),
                             _raw_stream(dev)), "moe_linear")
     return (y, z) if save else y
 
 
-@_operator
-def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=None, dw=None, workspace=None):
+def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=None, dw=None, workspace=None,
+                    stream=None):
     """moe_linear_backward: (dx bf16 [T,K], dw bf16 [N,K], db bf16 [N] or None)
     from dy [T,N], with x, w and, for an activation, the z that the forward
     kept. ``bias`` asks for db; the residual's gradient is dy itself.
     ``stream``: launch there."""
     a = _act(act, _LINEAR_ACT)
     shape, dev = _first(x, "x")
+    if _elsewhere(dev, stream):
+        with _on(x.device, stream):
+            return linear_backward(dy, x, w, z, act, bias, dx, dw, workspace)
     T, K = shape
     N = _rows(w, "w")
     wp = _tensor(w, "w", _BF16, (N, K), dev)
