@@ -559,7 +559,8 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
   int workers = num_sms / TL::kCtas;
   if (kPair) {
     // every pair of the persistent grid must be resident at once
-    const int maxc = max_active_clusters(reinterpret_cast<const void*>(kernel), 2, Epilogue<kMode>::kThreads, TL::kSmem);
+    const int maxc =
+        max_active_clusters(reinterpret_cast<const void*>(kernel), 2, Epilogue<kMode>::kThreads, TL::kSmem);
     if (maxc > 0) workers = std::min(workers, maxc);
   }
   p.full = p.tiles = static_cast<int>(tiles);

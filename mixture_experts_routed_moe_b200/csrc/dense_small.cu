@@ -20,7 +20,7 @@
 // last MMA to the end, 16 x 2048 -> 7168: 3.1 us with partials read through
 // distributed shared memory between two cluster barriers, 1.9 so).
 //
-// Warps: 0 TMA producer, 1 MMA issuer; then all eight send and add. Every wait
+// Warps: 0 TMA producer, 1 MMA issuer; then all send and add. Every wait
 // is bounded; a cluster with a wait that gave up writes NaN.
 #include <algorithm>
 #include <limits>
@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr int kThreads = 256;
+constexpr int kManyThreads = 512;  // for large partials: see threads_of
 constexpr int kA = kTileM * kBK * 2;  // 16 KB of weights a stage
 constexpr int kMaxStages = 12;
 constexpr int kTileTokens = 128;  // most tokens of a token tile
@@ -152,7 +153,7 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
     }
     write_outputs<kGated>(p, g[0], u[0], bi, re, t0 + t, n, aborted);
   };
-  for (int i = threadIdx.x; i < nt * per; i += kThreads) {
+  for (int i = threadIdx.x; i < nt * per; i += blockDim.x) {
     const uint2 bi = bias[0], re = res[0];
 #pragma unroll
     for (int k = 1; k < kAhead; ++k) {
@@ -160,7 +161,7 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
       res[k - 1] = res[k];
     }
     if (!kGated) {
-      const int j = i + kAhead * kThreads, t = j / per;
+      const int j = i + kAhead * static_cast<int>(blockDim.x), t = j / per;
       if (t < nt) load_addends(p, t0 + t, n0 + rank * own + (j - t * per) * 4, bias[kAhead - 1], res[kAhead - 1]);
     }
     step(i, bi, re);
@@ -168,7 +169,7 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
 }
 
 template <bool kAmn, bool kGated>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kManyThreads)
     dense_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const SmallParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -299,11 +300,11 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
   }
-  // All eight warps send the partial: two per TMEM lane quadrant, taking the
-  // blocks of 16 tokens in turn.
+  // All warps send the partial: two or four per TMEM lane quadrant, taking the blocks
+  // of 16 tokens in turn (the producer's and the issuer's last).
   __syncwarp();
   {
-    const int quad = warp & 3, first = warp >= 2 && warp < 6 ? 0 : 16;
+    const int warps = blockDim.x / 32, quad = warp & 3, first = 16 * ((warp + warps - 2) % warps / 4);
     const int r = quad * 32 + lane;
     const bool busy = first < p.n_pad;
     const bool got = busy && mbar_wait_bounded(tfull, 0, s_abort, s_status, p.timeout_ns) && *s_abort == 0;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads)
       const uint32_t dst = cluster_map(smem_u32(s_part + rank * nt * len + up * own + (ru - owner * own)),
                                        static_cast<uint32_t>(owner));
       const uint32_t bar = cluster_map(smem_u32(arrived), static_cast<uint32_t>(owner));
-      for (int c = first; c < p.n_pad; c += 32) {
+      for (int c = first; c < p.n_pad; c += 4 * warps) {
         uint32_t v[16];
         tmem_ld16(tb + c, v);
         tmem_ld_wait();
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads)
   if (!kGated) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = threadIdx.x + k * kThreads, per = own / 4, t = i / per;
+      const int i = threadIdx.x + k * static_cast<int>(blockDim.x), per = own / 4, t = i / per;
       bias[k] = res[k] = make_uint2(0u, 0u);
       if (t < nt) load_addends(p, t0 + t, n0 + rank * own + (i - t * per) * 4, bias[k], res[k]);
     }
@@ -364,11 +365,18 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Token tiles, rows of a unit and CTAs of a cluster.
+// Token tiles, rows of a unit, CTAs of a cluster, threads of a CTA.
 struct Plan {
-  int tile_t, tiles, rows, csize, ctas;
+  int tile_t, tiles, rows, csize, ctas, threads;
   double us;  // estimated time; infinite where the CTAs would not be resident together
 };
+
+// Sixteen warps where a CTA sends and adds a large partial (linear 2048 -> 7168 for 200
+// tokens 21.4 us with eight, 17.6 with sixteen, for 96 13.6 and 11.8); with small ones and
+// with the gated epilogue they cost up to 8%.
+int threads_of(const DenseGemm& g, int tile_t, int rows, int csize) {
+  return g.order != kGatedNT && tile_t * rows / csize >= 6000 ? kManyThreads : kThreads;
+}
 
 // The estimate, in us, fitted to sweeps on B200 (weights of 2048 x 1408 to 7168 x
 // 2048, 1 to 512 tokens, every shape): 2.1 for the launch, the first loads and
@@ -399,10 +407,11 @@ Plan plan_small(const DenseGemm& g, int num_sms) {
         const double share = ctas > num_sms ? 2 : 1;
         const double bytes = (gated ? 2 : 1) * rows * 128 + n_pad * 128;
         const double step = std::max({0.22, 0.94 / ring_stages(tile_t, n_pad), bytes / (share > 1 ? 86e3 : 266e3)});
+        const int threads = threads_of(g, tile_t, rows, c);
         const double us = 2.1 + (num_kb + c - 1) / c * step + 0.13 * c + 0.022 * tile_t +
-                          0.47 * tile_t * rows / c / 1024 + 0.36 * weights +
+                          (threads == kThreads ? 0.47 : 0.17) * tile_t * rows / c / 1024 + 0.36 * weights +
                           (share > 1 ? 1.1 + 0.16 * weights : 0.0);
-        if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), us};
+        if (us < best.us) best = Plan{tile_t, static_cast<int>(tiles), rows, c, static_cast<int>(ctas), threads, us};
       }
     }
   }
@@ -448,7 +457,7 @@ cudaError_t launch_t(const DenseGemm& g, int num_sms, cudaStream_t st) {
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(plan.threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(p.tile_t));
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
