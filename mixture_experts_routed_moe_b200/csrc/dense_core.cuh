@@ -79,39 +79,73 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The standard normal distribution function at z, and e = exp(-z^2 / 2):
+// Two fp32 values in one register pair: the packed multiply-add takes one issue slot for
+// both, and the epilogues' tail and the gradients' elementwise pass are paced by issue.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ Pair pair(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(Pair p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// The standard normal distribution function at two z, and e = exp(-z^2 / 2):
 // Phi(-|z|) = e/2 erfcx(|z| / sqrt 2), with erfcx(x) = e^(x^2) erfc(x) as a
 // polynomial of degree 7 without constant term in t = 1 / (1 + 0.375 x), the
 // form of Abramowitz and Stegun 7.1.26, fitted here by weighted least squares to
-// a relative error of 7e-7 on [0, 11]. The negative side keeps its relative
-// accuracy (4e-6 at z = -12), which 1 + erf(z / sqrt 2) loses from -4 on.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-  const float t = rcp_approx(fmaf(0.375f * 0.7071067811865476f, fabsf(z), 1.0f));
-  float q = -0.13459716737270355f;
-  q = fmaf(q, t, 0.386208713054657f);
-  q = fmaf(q, t, -0.12719842791557312f);
-  q = fmaf(q, t, 0.2813640832901001f);
-  q = fmaf(q, t, 0.16730797290802002f);
-  q = fmaf(q, t, 0.2155657857656479f);
-  q = fmaf(q, t, 0.2113487720489502f);
-  e = exp2_approx(z * z * (-0.5f * kLog2e));
-  const float tail = q * t * (0.5f * e);
-  return z >= 0.0f ? 1.0f - tail : tail;  // a NaN stays one
+// a relative error of 7e-7 on [0, 11] (its coefficients halved below). The negative
+// side keeps its relative accuracy (4e-6 at z = -12), which 1 + erf(z / sqrt 2) loses
+// from -4 on.
+__device__ __forceinline__ Pair normal_cdf(Pair z, Pair& e) {
+  float z0, z1, t0, t1;
+  split(z, z0, z1);
+  split(fma2(pair(0.375f * 0.7071067811865476f), pair(fabsf(z0), fabsf(z1)), pair(1.0f)), t0, t1);
+  const Pair t = pair(rcp_approx(t0), rcp_approx(t1));
+  Pair q = pair(0.5f * -0.13459716737270355f);
+  q = fma2(q, t, pair(0.5f * 0.386208713054657f));
+  q = fma2(q, t, pair(0.5f * -0.12719842791557312f));
+  q = fma2(q, t, pair(0.5f * 0.2813640832901001f));
+  q = fma2(q, t, pair(0.5f * 0.16730797290802002f));
+  q = fma2(q, t, pair(0.5f * 0.2155657857656479f));
+  q = fma2(q, t, pair(0.5f * 0.2113487720489502f));
+  split(mul2(mul2(z, z), pair(-0.5f * kLog2e)), t0, t1);
+  e = pair(exp2_approx(t0), exp2_approx(t1));
+  split(mul2(mul2(q, t), e), t0, t1);  // the tail
+  return pair(z0 >= 0.0f ? 1.0f - t0 : t0, z1 >= 0.0f ? 1.0f - t1 : t1);  // a NaN stays one
 }
 
-// The activation kAct (kActNone: the identity).
+// Two values through the activation kAct (kActNone: the identity).
 template <int kAct>
-__device__ __forceinline__ float act_t(float z) {
+__device__ __forceinline__ void act2(float& a, float& b) {
   if (kAct == MOE_ACT_GELU) {
-    float e;
-    return z * normal_cdf(z, e);
+    Pair e;
+    const Pair z = pair(a, b);
+    split(mul2(z, normal_cdf(z, e)), a, b);
+  } else if (kAct == MOE_ACT_RELU) {
+    a = a > 0.0f || a != a ? a : 0.0f;
+    b = b > 0.0f || b != b ? b : 0.0f;
+  } else if (kAct == MOE_ACT_SILU) {
+    a *= rcp_approx(1.0f + exp2_approx(a * -kLog2e));
+    b *= rcp_approx(1.0f + exp2_approx(b * -kLog2e));
   }
-  if (kAct == MOE_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;
-  if (kAct == MOE_ACT_SILU) return z * rcp_approx(1.0f + exp2_approx(z * -kLog2e));
-  return z;
 }
 
-// f = act(z) and d = act'(z):
+// f = act(z) and d = act'(z) of two values:
 //   silu z p, p (1 + z (1 - p)) with p = 1 / (1 + e^-z)
 //   gelu z Phi(z), Phi(z) + z e^(-z^2/2) / sqrt(2 pi)
 //   relu max(z, 0), [z > 0]
@@ -122,17 +156,24 @@ __device__ __forceinline__ void act_and_slope(float z, float& f, float& d) {
     const float p = rcp_approx(1.0f + exp2_approx(z * -kLog2e));
     f = z * p;
     d = p * fmaf(z, 1.0f - p, 1.0f);
-  } else if (kAct == MOE_ACT_GELU) {
-    float e;
-    const float q = normal_cdf(z, e);
-    f = z * q;
-    d = fmaf(z * 0.3989422804014327f, e, q);
   } else if (kAct == MOE_ACT_RELU) {
-    f = act_t<MOE_ACT_RELU>(z);
+    f = z > 0.0f || z != z ? z : 0.0f;
     d = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   } else {
     f = z;
     d = 1.0f;
+  }
+}
+template <int kAct>
+__device__ __forceinline__ void act_and_slope2(const float (&z)[2], float (&f)[2], float (&d)[2]) {
+  if (kAct == MOE_ACT_GELU) {
+    Pair e;
+    const Pair zz = pair(z[0], z[1]), q = normal_cdf(zz, e);
+    split(mul2(zz, q), f[0], f[1]);
+    split(fma2(mul2(zz, pair(0.3989422804014327f)), e, q), d[0], d[1]);
+  } else {
+    act_and_slope<kAct>(z[0], f[0], d[0]);
+    act_and_slope<kAct>(z[1], f[1], d[1]);
   }
 }
 

@@ -414,7 +414,11 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
           }
           with_act(p.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_t<decltype(tag)::value>(v[i]) * u[i];
+            for (int i = 0; i < 32; i += 2) {
+              act2<decltype(tag)::value>(v[i], v[i + 1]);
+              v[i] *= u[i];
+              v[i + 1] *= u[i + 1];
+            }
           });
         } else if (kMode == kModeBackward) {
           tmem_load32(tb + c, v);
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
           if (p.act != kActNone) {
             with_act(p.act, [&](auto tag) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = act_t<decltype(tag)::value>(v[i]);
+              for (int i = 0; i < 32; i += 2) act2<decltype(tag)::value>(v[i], v[i + 1]);
             });
           }
           if (p.residual != nullptr) {

@@ -6,7 +6,9 @@
 //   linear: dz = dy act'(z)                           -> bf16 [T, N]
 //           db = sum_t dz                             (from the fp32 dz)
 //
-// HBM-bound: 16-byte loads and stores, each element once. dg, du and dz are
+// HBM-bound: 16-byte loads and stores, each element once; gelu's slope is paced by issue
+// as much, so that it works on packed pairs (4096 x 14336 gated 129.8 -> 122.9 us, 6.7 TB/s;
+// dz and db 69.4 -> 62.8, there with the 16-byte loads; silu 126.6 and 57.8). dg, du and dz are
 // rounded to bf16 because they are the tensor cores' operands of the products
 // that follow; the column sums are fp32 in a fixed order.
 #include <algorithm>
@@ -16,7 +18,7 @@
 namespace moe {
 namespace {
 
-constexpr int kGradCols = 128;  // columns of a block of linear_grad_kernel
+constexpr int kGradCols = 256;  // columns of a block of linear_grad_kernel
 
 template <int kAct>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict__ gu,
@@ -40,68 +42,69 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const float* __restrict
     uint32_t og[4], ou[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float f0, s0, f1, s1;
-      act_and_slope<kAct>(g[2 * q], f0, s0);
-      act_and_slope<kAct>(g[2 * q + 1], f1, s1);
+      float f[2], s[2];
+      act_and_slope2<kAct>({g[2 * q], g[2 * q + 1]}, f, s);
       const float a = bf16_lo(dw[q]), b = bf16_hi(dw[q]);
-      og[q] = pack_bf16x2(a * u[2 * q] * s0, b * u[2 * q + 1] * s1);
-      ou[q] = pack_bf16x2(a * f0, b * f1);
+      og[q] = pack_bf16x2(a * u[2 * q] * s[0], b * u[2 * q + 1] * s[1]);
+      ou[q] = pack_bf16x2(a * f[0], b * f[1]);
     }
     *reinterpret_cast<uint4*>(dgu + 2 * t * I + c) = make_uint4(og[0], og[1], og[2], og[3]);
     *reinterpret_cast<uint4*>(dgu + 2 * t * I + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
   }
 }
 
-// Block (x, y): 128 columns (4 a lane of a warp), rows y, y + 8, ... by its
-// eight warps within the row range of blockIdx.y, four rows' loads in flight; dz
+// Block (x, y): 256 columns (8 a lane of a warp), rows y, y + 8, ... by its
+// eight warps within the row range of blockIdx.y, two rows' loads in flight; dz
 // written, the fp32 column sums of the range added over the warps in order and
 // left in partial[y].
 template <int kAct>
-__global__ void __launch_bounds__(256, 4) linear_grad_kernel(const __nv_bfloat16* __restrict__ z,
-                                                          const __nv_bfloat16* __restrict__ dy,
-                                                          __nv_bfloat16* __restrict__ dz, float* __restrict__ partial,
-                                                          long long T, int N) {
+__global__ void __launch_bounds__(256, 4)
+    linear_grad_kernel(const __nv_bfloat16* __restrict__ z, const __nv_bfloat16* __restrict__ dy,
+                       __nv_bfloat16* __restrict__ dz, float* __restrict__ partial, long long T, int N) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kRows = 4;
+  constexpr int kRows = 2;
   __shared__ float s_sum[8][kGradCols];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * kGradCols + lane * 4;
+  const int c = blockIdx.x * kGradCols + lane * 8;
   const long long t0 = blockIdx.y * T / gridDim.y, t1 = (blockIdx.y + 1) * T / gridDim.y;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  float sum[8] = {};
   if (c < N) {
     for (long long t = t0 + warp; t < t1; t += 8 * kRows) {
-      uint2 d[kRows], zz[kRows];
+      uint4 d[kRows], zz[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const size_t at = static_cast<size_t>(t + 8 * k) * N + c;
-        d[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint2*>(dy + at) : make_uint2(0u, 0u);
+        d[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint4*>(dy + at) : make_uint4(0u, 0u, 0u, 0u);
         if (kAct != kActNone)
-          zz[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint2*>(z + at) : make_uint2(0u, 0u);
+          zz[k] = t + 8 * k < t1 ? *reinterpret_cast<const uint4*>(z + at) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
-        float v[4] = {bf16_lo(d[k].x), bf16_hi(d[k].x), bf16_lo(d[k].y), bf16_hi(d[k].y)};
-        if (kAct != kActNone) {
-          const float zk[4] = {bf16_lo(zz[k].x), bf16_hi(zz[k].x), bf16_lo(zz[k].y), bf16_hi(zz[k].y)};
+        const uint32_t dw[4] = {d[k].x, d[k].y, d[k].z, d[k].w};
+        const uint32_t zw[4] = {zz[k].x, zz[k].y, zz[k].z, zz[k].w};
+        uint32_t o[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float f, s;
-            act_and_slope<kAct>(zk[q], f, s);
-            v[q] *= s;
+        for (int q = 0; q < 4; ++q) {
+          float v0 = bf16_lo(dw[q]), v1 = bf16_hi(dw[q]);
+          if (kAct != kActNone) {
+            float f[2], s[2];
+            act_and_slope2<kAct>({bf16_lo(zw[q]), bf16_hi(zw[q])}, f, s);
+            v0 *= s[0];
+            v1 *= s[1];
+            o[q] = pack_bf16x2(v0, v1);
           }
-          if (t + 8 * k < t1)
-            *reinterpret_cast<uint2*>(dz + static_cast<size_t>(t + 8 * k) * N + c) =
-                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+          sum[2 * q] += v0;
+          sum[2 * q + 1] += v1;
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum[q] += v[q];
+        if (kAct != kActNone && t + 8 * k < t1)
+          *reinterpret_cast<uint4*>(dz + static_cast<size_t>(t + 8 * k) * N + c) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
   if (partial == nullptr) return;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) s_sum[warp][lane * 4 + q] = sum[q];
+  for (int q = 0; q < 8; ++q) s_sum[warp][lane * 8 + q] = sum[q];
   __syncthreads();
   const int col = blockIdx.x * kGradCols + threadIdx.x;
   if (threadIdx.x < kGradCols && col < N) {
@@ -126,9 +129,9 @@ cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T,
 }
 
 int linear_grad_rows(int T, int N) {
-  // row ranges: one wave of four blocks an SM of a B200, at least 64 rows each
+  // row ranges: one wave of four blocks an SM of a B200, at least 16 rows each (two a warp)
   const int cols = (N + kGradCols - 1) / kGradCols;
-  return std::max(1, std::min((T + 63) / 64, std::max(1, 592 / cols)));
+  return std::max(1, std::min((T + 15) / 16, std::max(1, 592 / cols)));
 }
 
 cudaError_t launch_linear_grad(const void* z, const void* dy, void* dz, float* partial, void* db, int T, int N,

@@ -90,11 +90,13 @@ __device__ __forceinline__ void write_outputs(const SmallParams& p, float4 z, fl
   }
   with_act(p.act, [&](auto tag) {
     constexpr int kAct = decltype(tag)::value;
-    v[0] = act_t<kAct>(z.x);
-    v[1] = act_t<kAct>(z.y);
-    v[2] = act_t<kAct>(z.z);
-    v[3] = act_t<kAct>(z.w);
+    act2<kAct>(z.x, z.y);
+    act2<kAct>(z.z, z.w);
   });
+  v[0] = z.x;
+  v[1] = z.y;
+  v[2] = z.z;
+  v[3] = z.w;
   if (kGated) {
     v[0] *= u.x;
     v[1] *= u.y;

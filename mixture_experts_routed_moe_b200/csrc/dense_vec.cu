@@ -143,32 +143,47 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) dense_vec_kernel(const VecP
     z[2] += v.z;
     z[3] += v.w;
   }
+  // z: tokens 2c and 2c + 1 of row g, then of row g + 8
+  const int t0 = 8 * warp + 2 * c;
+  const int n = n0 + g;
+  if constexpr (kGated) {
+    if (p.save != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = 8 * warp + 2 * c + i;
-    if (t >= p.T) continue;
-    if constexpr (kGated) {
-      const int n = n0 + g;
-      if (p.save != nullptr) {
-        float* gu = static_cast<float*>(p.save) + static_cast<size_t>(t) * 2 * p.N + n;
+      for (int i = 0; i < 2; ++i) {
+        if (t0 + i >= p.T) continue;
+        float* gu = static_cast<float*>(p.save) + static_cast<size_t>(t0 + i) * 2 * p.N + n;
         gu[0] = z[i];
         gu[p.N] = z[2 + i];
       }
-      p.out[static_cast<size_t>(t) * p.N + n] = __float2bfloat16_rn(
-          with_act(p.act, [&](auto tag) { return act_t<decltype(tag)::value>(z[i]) * z[2 + i]; }));
-    } else {
+    }
+    with_act(p.act, [&](auto tag) { act2<decltype(tag)::value>(z[0], z[1]); });
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 1 && !two) break;
-        const int n = n0 + 8 * h + g;
-        const size_t o = static_cast<size_t>(t) * p.N + n;
-        float y = z[2 * h + i];
-        if (p.bias != nullptr) y += __bfloat162float(p.bias[n]);
-        if (p.save != nullptr) static_cast<__nv_bfloat16*>(p.save)[o] = __float2bfloat16_rn(y);
-        y = with_act(p.act, [&](auto tag) { return act_t<decltype(tag)::value>(y); });
+    for (int i = 0; i < 2; ++i)
+      if (t0 + i < p.T) p.out[static_cast<size_t>(t0 + i) * p.N + n] = __float2bfloat16_rn(z[i] * z[2 + i]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && !two) break;
+      const int m = n + 8 * h;
+      const size_t o = static_cast<size_t>(t0) * p.N + m;
+      float y[2] = {z[2 * h], z[2 * h + 1]};
+      if (p.bias != nullptr) {
+        const float b = __bfloat162float(p.bias[m]);
+        y[0] += b;
+        y[1] += b;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (p.save != nullptr && t0 + i < p.T)
+          static_cast<__nv_bfloat16*>(p.save)[o + i * static_cast<size_t>(p.N)] = __float2bfloat16_rn(y[i]);
+      with_act(p.act, [&](auto tag) { act2<decltype(tag)::value>(y[0], y[1]); });
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (t0 + i >= p.T) continue;
+        const size_t at = o + i * static_cast<size_t>(p.N);
         // (not one FMA with the activation's last product: the bits are those of a call with save)
-        if (p.residual != nullptr) y = __fadd_rn(y, __bfloat162float(p.residual[o]));
-        p.out[o] = __float2bfloat16_rn(y);
+        if (p.residual != nullptr) y[i] = __fadd_rn(y[i], __bfloat162float(p.residual[at]));
+        p.out[at] = __float2bfloat16_rn(y[i]);
       }
     }
   }
