@@ -80,7 +80,7 @@ def _rows(t, name):
 
 def _workspace(ws, need, like):
     if ws is None:
-        return like.new_empty(need, dtype=torch.uint8)
+        return like.new_empty(need // 2)  # (bf16, as `like` is; sizes are multiples of 256 bytes)
     _need(ws, "workspace", (torch.uint8,), 1, cuda=False)
     if ws.device != like.device:
         raise ValueError(f"workspace is on {ws.device}, not {like.device}: all tensors must share one CUDA device")
@@ -155,7 +155,7 @@ def rms_norm_backward(dy, s, weight, rstd, dresidual=None, dx=None, dw=None, wor
     dw, dwp = _output(dw, "dw", weight, (H,), dev)
     L = lib()
     ws = _workspace(workspace, L.moe_rms_norm_backward_workspace_size(T, H), dy)
-    _check(L.moe_rms_norm_backward(dy.data_ptr(), sp, w, r, dr, T, H, dxp, dwp, ws.data_ptr(), ws.numel(),
+    _check(L.moe_rms_norm_backward(dy.data_ptr(), sp, w, r, dr, T, H, dxp, dwp, ws.data_ptr(), ws.nbytes,
                                    _raw_stream(dev)), "moe_rms_norm_backward")
     return dx, dw
 
@@ -202,7 +202,7 @@ def gated_ffn_backward(dh, x, w_gate_up, gu, act: str = "silu", dx=None, dw=None
     dw, dwp = _output(dw, "dw", w_gate_up, (2 * I, H), dev)
     L = lib()
     ws = _workspace(workspace, L.moe_gated_ffn_backward_workspace_size(T, I), x)
-    _check(L.moe_gated_ffn_backward(d, x.data_ptr(), w, g, T, H, I, a, dxp, dwp, ws.data_ptr(), ws.numel(),
+    _check(L.moe_gated_ffn_backward(d, x.data_ptr(), w, g, T, H, I, a, dxp, dwp, ws.data_ptr(), ws.nbytes,
                                     _raw_stream(dev)), "moe_gated_ffn_backward")
     return dx, dw
 
@@ -251,5 +251,5 @@ def linear_backward(dy, x, w, z=None, act: str = "none", bias: bool = False, dx=
     L = lib()
     ws = _workspace(workspace, L.moe_linear_backward_workspace_size(T, N, a, int(bool(bias))), x)
     _check(L.moe_linear_backward(d, x.data_ptr(), wp, zp, T, K, N, a, dxp, dwp, None if db is None else db.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), _raw_stream(dev)), "moe_linear_backward")
+                                 ws.data_ptr(), ws.nbytes, _raw_stream(dev)), "moe_linear_backward")
     return dx, dw, db
