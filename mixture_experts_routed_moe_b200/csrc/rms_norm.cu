@@ -154,6 +154,17 @@ __device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, 
   return s;
 }
 
+// Blocks of kMaxThreads an SM that the registers are bounded for, and so the threads that
+// the grid may count on. (With the bound left at one block, codes at 70 registers a thread
+// let 1024-thread grids run in two rounds: 8192 x 2048 35.6 us against 25.7.) Without a residual a row
+// has half the bytes, so that more rows have to be in flight (13.4 us with 1536 threads,
+// 17.1 with 1024); 640 threads are rows of 4104 to 5120 columns, two an SM.
+constexpr int norm_residency(int vec, int threads, bool res) {
+  if (threads == 640) return 2;
+  if (threads != 512 || vec > 2) return 1;
+  return vec == 1 && !res ? 3 : 2;
+}
+
 // A row is held by `tpr` threads: one warp, with blockDim / 32 rows in a
 // block, or the whole block. Thread i of the row holds the 16-byte vectors i,
 // i + tpr, ...; the 16 vectors of a 128-column group lie in one half-warp. The
@@ -166,7 +177,7 @@ __device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, 
 // of rows through a ring in shared memory (3 to 6 stages) measured 24 to 30 us
 // on the first, one block a row without the walk 26.
 template <int kVec, int kMaxThreads, bool kRes, bool kCodes>
-__global__ void __launch_bounds__(kMaxThreads, !kRes && kVec == 1 && kMaxThreads == 512 ? 3 : 1)
+__global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads, kRes))
     rms_norm_kernel(const NormParams p, int tpr) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
@@ -369,10 +380,6 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
   }
 }
 
-// Threads of the norm's grid per SM. Without a residual a row has half the bytes,
-// so more rows have to be in flight (8192 x 2048: 13.4 us with 1536 threads, 17.1 with 1024).
-constexpr int norm_threads(bool res) { return res ? 1024 : 1536; }
-
 int round32(int v) { return (v + 31) / 32 * 32; }
 
 }  // namespace
@@ -384,18 +391,25 @@ cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* ou
 
 namespace {
 
+template <int kVec, int kMaxThreads, bool kRes, bool kCodes>
+cudaError_t launch_norm_k(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
+  const long long rpb = block / tpr;
+  // as many blocks as are resident; four vectors with a residual run in two rounds, whose
+  // first loads overlap the others' last rows (4096 x 8192 43.3 us against 46.0)
+  const int fit = kVec == 4 && kRes && !kCodes ? 1024 : kMaxThreads * norm_residency(kVec, kMaxThreads, kRes);
+  const int per_sm = std::max(1, fit / block);
+  const long long blocks = std::min<long long>((p.T + rpb - 1) / rpb, static_cast<long long>(num_sms) * per_sm);
+  return launch_pdl(rms_norm_kernel<kVec, kMaxThreads, kRes, kCodes>, dim3(static_cast<unsigned>(blocks)),
+                    dim3(static_cast<unsigned>(block)), 0, st, p, tpr);
+}
+
 template <int kVec, int kMaxThreads>
 cudaError_t launch_norm_t(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
-  const long long rpb = block / tpr;
-  const int per_sm = std::max(1, norm_threads(p.residual != nullptr) / block);
-  const long long blocks = std::min<long long>((p.T + rpb - 1) / rpb, static_cast<long long>(num_sms) * per_sm);
-  const dim3 grid(static_cast<unsigned>(blocks));
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(static_cast<unsigned>(block)), 0, st, p, tpr); };
   if (p.residual != nullptr)
-    return p.codes != nullptr ? go(rms_norm_kernel<kVec, kMaxThreads, true, true>)
-                              : go(rms_norm_kernel<kVec, kMaxThreads, true, false>);
-  return p.codes != nullptr ? go(rms_norm_kernel<kVec, kMaxThreads, false, true>)
-                            : go(rms_norm_kernel<kVec, kMaxThreads, false, false>);
+    return p.codes != nullptr ? launch_norm_k<kVec, kMaxThreads, true, true>(p, block, tpr, num_sms, st)
+                              : launch_norm_k<kVec, kMaxThreads, true, false>(p, block, tpr, num_sms, st);
+  return p.codes != nullptr ? launch_norm_k<kVec, kMaxThreads, false, true>(p, block, tpr, num_sms, st)
+                            : launch_norm_k<kVec, kMaxThreads, false, false>(p, block, tpr, num_sms, st);
 }
 
 }  // namespace
@@ -426,6 +440,9 @@ cudaError_t launch_rms_norm(const void* x, const void* residual, const void* wei
   // (16 x 7168 with codes: 2.8 us against 3.7 with four) and where the codes'
   // arithmetic paces it (4096 x 7168: 47.0 against 48.1); four keep more bytes
   // in flight (4096 x 7168 without codes: 37.6 us against 43).
+  // (two blocks an SM where they fit: 4096 x 5120 with codes 31.9 us against 37.8)
+  if (nvec <= 640 && codes != nullptr && T > 2 * num_sms)
+    return launch_norm_t<1, 640>(p, threads(1), threads(1), num_sms, st);
   if (nvec <= 1024 && (codes != nullptr || T <= 2 * num_sms))
     return launch_norm_t<1, 1024>(p, threads(1), threads(1), num_sms, st);
   if (nvec <= 2048) return launch_norm_t<4, 512>(p, threads(4), threads(4), num_sms, st);
