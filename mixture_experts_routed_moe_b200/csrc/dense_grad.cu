@@ -7,8 +7,9 @@
 //           db = sum_t dz                             (from the fp32 dz)
 //
 // HBM-bound: 16-byte loads and stores, each element once; gelu's slope is paced by issue
-// as much, so that it works on packed pairs (4096 x 14336 gated 129.8 -> 122.9 us, 6.7 TB/s;
-// dz and db 69.4 -> 62.8, there with the 16-byte loads; silu 126.6 and 57.8). dg, du and dz are
+// as much, so that it works on packed pairs (4096 x 14336 gated 7 us less, now 115 = 7.2 TB/s
+// with the last writes still in L2, silu 117; dz and db 69.4 -> 62.8, there with the
+// 16-byte loads, silu 57.8). dg, du and dz are
 // rounded to bf16 because they are the tensor cores' operands of the products
 // that follow; the column sums are fp32 in a fixed order.
 #include <algorithm>
@@ -120,7 +121,8 @@ __global__ void __launch_bounds__(256, 4)
 cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T, int I, int act, int num_sms,
                               cudaStream_t st) {
   const long long n = static_cast<long long>(T) * (I / 8);
-  const long long blocks = std::min<long long>((n + 255) / 256, static_cast<long long>(num_sms) * 8);
+  // a thread a vector (4096 x 14336: 117 us; one wave of blocks that walk 126)
+  const long long blocks = std::min<long long>((n + 255) / 256, static_cast<long long>(num_sms) * 256);
   return with_act(act, [&](auto tag) {
     return launch_pdl(gated_grad_kernel<decltype(tag)::value>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
                       gu, static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dgu),
