@@ -42,7 +42,8 @@ def test_rms_norm(T, H, residual):
 
 
 @pytest.mark.parametrize("T,H", [(1, 128), (16, 2048), (77, 7168), (3, 1152), (130, 4096), (1, 65536),
-                                 (2500, 2048), (700, 7168), (500, 16384)])
+                                 (2500, 2048), (700, 7168), (500, 16384),
+                                 (700, 4224), (500, 5120), (1300, 1024), (900, 2048)])
 def test_rms_norm_codes(T, H):
     x, w, r = normal(1, T, H), normal(2, H, std=0.2, mean=1.0), normal(3, T, H)
     x[0, :128] = 0
