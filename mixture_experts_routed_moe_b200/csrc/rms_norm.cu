@@ -97,7 +97,7 @@ struct RowSum {
 };
 
 // Scales one thread's vectors of row t and writes y, the codes and the scales.
-template <int kVec, bool kCodes>
+template <int kVec, bool kCodes, bool kLean>
 __device__ __forceinline__ void norm_write(const NormParams& p, const uint4 (&s)[kVec], const uint4 (&w)[kVec], float r,
                                            size_t base, int i0, int tpr, int nvec) {
   const unsigned hmask = 0xFFFFu << (threadIdx.x & 16);
@@ -107,7 +107,7 @@ __device__ __forceinline__ void norm_write(const NormParams& p, const uint4 (&s)
     if (i >= nvec) continue;  // H % 128 == 0 with codes: whole half-warps skip
     float a[8], g[8];
     unpack8(s[j], a);
-    unpack8(w[j], g);
+    unpack8(kLean ? __ldg(reinterpret_cast<const uint4*>(p.weight) + i) : w[j], g);
 #pragma unroll
     for (int q = 0; q < 8; ++q) a[q] = a[q] * r * g[q];
     if (!kCodes || p.y != nullptr) reinterpret_cast<uint4*>(p.y + base)[i] = pack8(a);
@@ -159,7 +159,8 @@ __device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, 
 // let 1024-thread grids run in two rounds: 8192 x 2048 35.6 us against 25.7.) Without a residual a row
 // has half the bytes, so that more rows have to be in flight (13.4 us with 1536 threads,
 // 17.1 with 1024); 640 threads are rows of 4104 to 5120 columns, two an SM.
-constexpr int norm_residency(int vec, int threads, bool res) {
+constexpr int norm_residency(int vec, int threads, bool res, bool lean) {
+  if (lean) return threads <= 256 ? 4 : threads <= 320 ? 3 : 2;
   if (threads == 640) return 2;
   if (threads != 512 || vec > 2) return 1;
   return vec == 1 && !res ? 3 : 2;
@@ -171,13 +172,16 @@ constexpr int norm_residency(int vec, int threads, bool res) {
 // grid is a few blocks an SM; each row group walks over its rows with the next
 // row's loads in flight while it reduces and stores the current one.
 //
+// kLean: the weights are read again for every row, from L1, and beyond 6144 columns the
+// next row's loads go out after the sum: registers for one more block an SM.
+//
 // Measured on B200 (CUDA graph, inputs from HBM): 8192 x 2048 with a residual
 // 22.9 us = 5.86 TB/s, 0.89 of the measured copy bandwidth; 4096 x 8192 43.4 us =
-// 6.18 TB/s; 4096 x 7168 with codes 47.4 us = 5.59 TB/s; one row 1.7 us. Bulk copies
+// 6.18 TB/s; 4096 x 7168 with codes 43.7 us = 6.05 TB/s; one row 1.7 us. Bulk copies
 // of rows through a ring in shared memory (3 to 6 stages) measured 24 to 30 us
 // on the first, one block a row without the walk 26.
-template <int kVec, int kMaxThreads, bool kRes, bool kCodes>
-__global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads, kRes))
+template <int kVec, int kMaxThreads, bool kRes, bool kCodes, bool kLean>
+__global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads, kRes, kLean))
     rms_norm_kernel(const NormParams p, int tpr) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
@@ -186,6 +190,7 @@ __global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads,
   const RowSum<kVec> row_sum(tpr);
   const int i0 = threadIdx.x % tpr;
   const int nvec = p.H / 8;
+  constexpr bool kLate = kLean && kMaxThreads > 384;  // (before the sum at 6144 columns: 38.1 us, after it 38.6)
   const long long step = static_cast<long long>(gridDim.x) * rpb;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   uint4 w[kVec], xv[kVec], rv[kVec];
@@ -219,11 +224,12 @@ __global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads,
       const int i = i0 + j * tpr;
       if (kRes && p.residual_out != nullptr && i < nvec) reinterpret_cast<uint4*>(p.residual_out + base)[i] = s[j];
     }
-    if (t + step < p.T) load(t + step);
+    if (!kLate && t + step < p.T) load(t + step);
     const float sum = row_sum(sq, s_red[flip]);
     const float r = rsqrtf(fmaf(sum, inv_h, p.eps));
+    if (kLate && t + step < p.T) load(t + step);
     if (p.rstd != nullptr && i0 == 0) p.rstd[t] = r;
-    norm_write<kVec, kCodes>(p, s, w, r, base, i0, tpr, nvec);
+    norm_write<kVec, kCodes, kLean>(p, s, w, r, base, i0, tpr, nvec);
   }
 }
 
@@ -391,25 +397,32 @@ cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* ou
 
 namespace {
 
-template <int kVec, int kMaxThreads, bool kRes, bool kCodes>
+template <int kVec, int kMaxThreads, bool kLean, bool kRes, bool kCodes>
 cudaError_t launch_norm_k(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
   const long long rpb = block / tpr;
   // as many blocks as are resident; four vectors with a residual run in two rounds, whose
   // first loads overlap the others' last rows (4096 x 8192 43.3 us against 46.0)
-  const int fit = kVec == 4 && kRes && !kCodes ? 1024 : kMaxThreads * norm_residency(kVec, kMaxThreads, kRes);
+  const int fit = kVec == 4 && kRes && !kCodes ? 1024 : kMaxThreads * norm_residency(kVec, kMaxThreads, kRes, kLean);
   const int per_sm = std::max(1, fit / block);
   const long long blocks = std::min<long long>((p.T + rpb - 1) / rpb, static_cast<long long>(num_sms) * per_sm);
-  return launch_pdl(rms_norm_kernel<kVec, kMaxThreads, kRes, kCodes>, dim3(static_cast<unsigned>(blocks)),
+  return launch_pdl(rms_norm_kernel<kVec, kMaxThreads, kRes, kCodes, kLean>, dim3(static_cast<unsigned>(blocks)),
                     dim3(static_cast<unsigned>(block)), 0, st, p, tpr);
 }
 
 template <int kVec, int kMaxThreads>
 cudaError_t launch_norm_t(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
   if (p.residual != nullptr)
-    return p.codes != nullptr ? launch_norm_k<kVec, kMaxThreads, true, true>(p, block, tpr, num_sms, st)
-                              : launch_norm_k<kVec, kMaxThreads, true, false>(p, block, tpr, num_sms, st);
-  return p.codes != nullptr ? launch_norm_k<kVec, kMaxThreads, false, true>(p, block, tpr, num_sms, st)
-                            : launch_norm_k<kVec, kMaxThreads, false, false>(p, block, tpr, num_sms, st);
+    return p.codes != nullptr ? launch_norm_k<kVec, kMaxThreads, false, true, true>(p, block, tpr, num_sms, st)
+                              : launch_norm_k<kVec, kMaxThreads, false, true, false>(p, block, tpr, num_sms, st);
+  return p.codes != nullptr ? launch_norm_k<kVec, kMaxThreads, false, false, true>(p, block, tpr, num_sms, st)
+                            : launch_norm_k<kVec, kMaxThreads, false, false, false>(p, block, tpr, num_sms, st);
+}
+
+// The lean form with codes, one row a block.
+template <int kMaxThreads>
+cudaError_t launch_norm_lean(const NormParams& p, int threads, int num_sms, cudaStream_t st) {
+  return p.residual != nullptr ? launch_norm_k<2, kMaxThreads, true, true, true>(p, threads, threads, num_sms, st)
+                               : launch_norm_k<2, kMaxThreads, true, false, true>(p, threads, threads, num_sms, st);
 }
 
 }  // namespace
@@ -435,15 +448,26 @@ cudaError_t launch_rms_norm(const void* x, const void* residual, const void* wei
   if (nvec <= 64) return launch_norm_t<2, 512>(p, 128, 32, num_sms, st);
   if (nvec <= 128) return launch_norm_t<4, 512>(p, 128, 32, num_sms, st);
   auto threads = [&](int vec) { return round32((nvec + vec - 1) / vec); };
+  // Codes over many rows: two vectors a thread in the lean form, where half the threads a row
+  // and few registers let two to four rows run on an SM and cover one another's waits
+  // (4096 x 7168 47.2 -> 43.7 us, 8192 columns 52.1 -> 50.1; without residual 35.1 -> 31.7, 4096
+  // columns 22.2 -> 18.5); with a residual up to 5120 columns one vector is as fast or
+  // faster (8192 x 2048 25.7 us against 27.8, 4096 x 5120 31.9 against 33.9).
+  if (codes != nullptr && T > 2 * num_sms) {
+    const int one = threads(1), two = threads(2);
+    if (nvec <= 640 && residual == nullptr)
+      return nvec <= 512 ? launch_norm_k<2, 256, true, false, true>(p, two, two, num_sms, st)
+                         : launch_norm_k<2, 320, true, false, true>(p, two, two, num_sms, st);
+    if (nvec > 512 && nvec <= 640) return launch_norm_k<1, 640, false, true, true>(p, one, one, num_sms, st);
+    if (nvec > 640 && nvec <= 768) return launch_norm_lean<384>(p, two, num_sms, st);
+    if (nvec > 768 && nvec <= 896) return launch_norm_lean<448>(p, two, num_sms, st);
+    if (nvec > 896 && nvec <= 1024) return launch_norm_lean<512>(p, two, num_sms, st);
+  }
   if (nvec <= 512) return launch_norm_t<1, 512>(p, threads(1), threads(1), num_sms, st);
   // One vector a thread shortens a row's path, which counts where few rows run
-  // (16 x 7168 with codes: 2.8 us against 3.7 with four) and where the codes'
-  // arithmetic paces it (4096 x 7168: 47.0 against 48.1); four keep more bytes
+  // (16 x 7168 with codes: 2.8 us against 3.7 with four); four keep more bytes
   // in flight (4096 x 7168 without codes: 37.6 us against 43).
-  // (two blocks an SM where they fit: 4096 x 5120 with codes 31.9 us against 37.8)
-  if (nvec <= 640 && codes != nullptr && T > 2 * num_sms)
-    return launch_norm_t<1, 640>(p, threads(1), threads(1), num_sms, st);
-  if (nvec <= 1024 && (codes != nullptr || T <= 2 * num_sms))
+  if (nvec <= 1024 && T <= 2 * num_sms)
     return launch_norm_t<1, 1024>(p, threads(1), threads(1), num_sms, st);
   if (nvec <= 2048) return launch_norm_t<4, 512>(p, threads(4), threads(4), num_sms, st);
   return launch_norm_t<8, 1024>(p, threads(8), threads(8), num_sms, st);

@@ -43,11 +43,14 @@ def test_rms_norm(T, H, residual):
 
 @pytest.mark.parametrize("T,H", [(1, 128), (16, 2048), (77, 7168), (3, 1152), (130, 4096), (1, 65536),
                                  (2500, 2048), (700, 7168), (500, 16384),
-                                 (700, 4224), (500, 5120), (1300, 1024), (900, 2048)])
-def test_rms_norm_codes(T, H):
+                                 (700, 4224), (500, 5120), (1300, 1024), (900, 2048), (1500, 1152), (800, 4096),
+                                 (400, 5248), (390, 6144), (333, 8192), (310, 8320)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_rms_norm_codes(T, H, residual):
     x, w, r = normal(1, T, H), normal(2, H, std=0.2, mean=1.0), normal(3, T, H)
     x[0, :128] = 0
     r[0, :128] = 0  # an all-zero group: scale 1, codes 0
+    r = r if residual else None
     n = moe.rms_norm(x, w, residual=r, eps=1e-6, quantize=True)
     plain = moe.rms_norm(x, w, residual=r, eps=1e-6)
     assert torch.equal(n.y, plain.y) and torch.equal(n.residual, plain.residual)
