@@ -156,9 +156,9 @@ __device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, 
 
 // Blocks of kMaxThreads an SM that the registers are bounded for, and so the threads that
 // the grid may count on. (With the bound left at one block, codes at 70 registers a thread
-// let 1024-thread grids run in two rounds: 8192 x 2048 35.6 us against 25.7.) Without a residual a row
-// has half the bytes, so that more rows have to be in flight (13.4 us with 1536 threads,
-// 17.1 with 1024); 640 threads are rows of 4104 to 5120 columns, two an SM.
+// let 1024-thread grids run in two rounds: 8192 x 2048 35.6 us against 25.7.) Without a
+// residual a row has half the bytes, so that more rows have to be in flight (13.4 us with
+// 1536 threads, 17.1 with 1024); 640 threads are rows of 4104 to 5120 columns, two an SM.
 constexpr int norm_residency(int vec, int threads, bool res, bool lean) {
   if (lean) return threads <= 256 ? 4 : threads <= 320 ? 3 : 2;
   if (threads == 640) return 2;
