@@ -27,7 +27,7 @@ struct NormParams {
   const __nv_bfloat16* residual;  // or null
   const __nv_bfloat16* weight;
   __nv_bfloat16* y;             // or null
-  __nv_bfloat16* residual_out;  // or null
+  __nv_bfloat16* residual_out;  // s, or null
   uint8_t* codes;               // or null
   float* scales;
   float* rstd;  // or null
@@ -134,6 +134,12 @@ __device__ __forceinline__ void norm_write(const NormParams& p, const uint4 (&s)
   }
 }
 
+// Where the residual stream s comes from, and whether it is written. kAlone: s is x, which
+// the caller keeps (the test for a buffer alone cost these forms up to 7%: 8192 x 2048
+// 13.3 us against 14.3); kCopied: s is x, written to a buffer of its own; kAdded: x +
+// residual, written where it is wanted.
+enum Stream { kAlone, kCopied, kAdded };
+
 // s = x + residual rounded to bf16 (x where the row has none), and the sum of its squares.
 template <bool kRes>
 __device__ __forceinline__ uint4 add_residual(const uint4& x, const uint4& res, float& sum) {
@@ -180,11 +186,12 @@ constexpr int norm_residency(int vec, int threads, bool res, bool lean) {
 // 6.18 TB/s; 4096 x 7168 with codes 43.7 us = 6.05 TB/s; one row 1.7 us. Bulk copies
 // of rows through a ring in shared memory (3 to 6 stages) measured 24 to 30 us
 // on the first, one block a row without the walk 26.
-template <int kVec, int kMaxThreads, bool kRes, bool kCodes, bool kLean>
-__global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads, kRes, kLean))
+template <int kVec, int kMaxThreads, int kStream, bool kCodes, bool kLean>
+__global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads, kStream == kAdded, kLean))
     rms_norm_kernel(const NormParams p, int tpr) {
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
+  constexpr bool kRes = kStream == kAdded;
   __shared__ float s_red[2][32 * kVec];
   const int rpb = blockDim.x / tpr;
   const RowSum<kVec> row_sum(tpr);
@@ -222,7 +229,8 @@ __global__ void __launch_bounds__(kMaxThreads, norm_residency(kVec, kMaxThreads,
     for (int j = 0; j < kVec; ++j) {
       s[j] = add_residual<kRes>(xv[j], rv[j], sq[j]);
       const int i = i0 + j * tpr;
-      if (kRes && p.residual_out != nullptr && i < nvec) reinterpret_cast<uint4*>(p.residual_out + base)[i] = s[j];
+      if (kStream != kAlone && p.residual_out != nullptr && i < nvec)
+        reinterpret_cast<uint4*>(p.residual_out + base)[i] = s[j];
     }
     if (!kLate && t + step < p.T) load(t + step);
     const float sum = row_sum(sq, s_red[flip]);
@@ -397,16 +405,28 @@ cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* ou
 
 namespace {
 
-template <int kVec, int kMaxThreads, bool kLean, bool kRes, bool kCodes>
-cudaError_t launch_norm_k(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
+template <int kVec, int kMaxThreads, bool kLean, int kStream, bool kCodes>
+cudaError_t launch_norm_s(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
+  constexpr bool kRes = kStream == kAdded;
   const long long rpb = block / tpr;
   // as many blocks as are resident; four vectors with a residual run in two rounds, whose
   // first loads overlap the others' last rows (4096 x 8192 43.3 us against 46.0)
   const int fit = kVec == 4 && kRes && !kCodes ? 1024 : kMaxThreads * norm_residency(kVec, kMaxThreads, kRes, kLean);
   const int per_sm = std::max(1, fit / block);
   const long long blocks = std::min<long long>((p.T + rpb - 1) / rpb, static_cast<long long>(num_sms) * per_sm);
-  return launch_pdl(rms_norm_kernel<kVec, kMaxThreads, kRes, kCodes, kLean>, dim3(static_cast<unsigned>(blocks)),
+  return launch_pdl(rms_norm_kernel<kVec, kMaxThreads, kStream, kCodes, kLean>, dim3(static_cast<unsigned>(blocks)),
                     dim3(static_cast<unsigned>(block)), 0, st, p, tpr);
+}
+
+template <int kVec, int kMaxThreads, bool kLean, bool kRes, bool kCodes>
+cudaError_t launch_norm_k(const NormParams& p, int block, int tpr, int num_sms, cudaStream_t st) {
+  if constexpr (kRes) {
+    return launch_norm_s<kVec, kMaxThreads, kLean, kAdded, kCodes>(p, block, tpr, num_sms, st);
+  } else {
+    return p.residual_out != nullptr
+               ? launch_norm_s<kVec, kMaxThreads, kLean, kCopied, kCodes>(p, block, tpr, num_sms, st)
+               : launch_norm_s<kVec, kMaxThreads, kLean, kAlone, kCodes>(p, block, tpr, num_sms, st);
+  }
 }
 
 template <int kVec, int kMaxThreads>
@@ -435,7 +455,8 @@ cudaError_t launch_rms_norm(const void* x, const void* residual, const void* wei
   p.residual = static_cast<const __nv_bfloat16*>(residual);
   p.weight = static_cast<const __nv_bfloat16*>(weight);
   p.y = static_cast<__nv_bfloat16*>(y);
-  p.residual_out = static_cast<__nv_bfloat16*>(residual_out);
+  // (without a residual the stream is x: only a buffer of its own has to be written)
+  p.residual_out = residual == nullptr && residual_out == x ? nullptr : static_cast<__nv_bfloat16*>(residual_out);
   p.codes = codes;
   p.scales = scales;
   p.rstd = rstd;
