@@ -95,12 +95,12 @@ def _act(act, table):
 
 class RMSNormOutput(typing.NamedTuple):
     """What ``rms_norm`` gives: ``y`` bf16 [T,H]; ``residual`` the residual
-    stream after the addition (x itself when no residual was given); with
-    quantize, ``codes`` float8_e4m3fn [T,H] and ``scales`` fp32 [T,H/128]; with
-    rstd, ``rstd`` fp32 [T] for ``rms_norm_backward``."""
+    stream after the addition (x itself when no residual was given, None when y
+    took its place); with quantize, ``codes`` float8_e4m3fn [T,H] and ``scales``
+    fp32 [T,H/128]; with rstd, ``rstd`` fp32 [T] for ``rms_norm_backward``."""
 
     y: torch.Tensor | None
-    residual: torch.Tensor
+    residual: torch.Tensor | None
     codes: torch.Tensor | None = None
     scales: torch.Tensor | None = None
     rstd: torch.Tensor | None = None
@@ -110,8 +110,9 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
              residual_out=None, stream=None) -> RMSNormOutput:
     """moe_rms_norm: s = x + residual (rounded to bf16, the residual stream),
     y = s * (mean(s^2) + eps)^(-1/2) * weight. ``out`` and ``residual_out`` may be
-    x or residual for an in-place step. ``quantize`` adds y in the form of the
-    FP8 experts' activations (H a multiple of 128). ``stream``: launch there."""
+    x or residual for an in-place step (without a residual, out = x overwrites the
+    stream: the result's ``residual`` is None then). ``quantize`` adds y in the form
+    of the FP8 experts' activations (H a multiple of 128). ``stream``: launch there."""
     shape, dev = _first(x, "x")
     if _elsewhere(dev, stream):
         with _on(x.device, stream):
@@ -125,7 +126,10 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
         s, sp = _output(residual_out, "residual_out", x, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out was given without a residual")
+    xp = x.data_ptr()
     y, yp = _output(out, "out", x, shape, dev)
+    if yp == xp and residual is None and T:
+        s = None  # x holds y after the call
     if quantize:
         codes = torch.empty_like(x, dtype=_FLOAT8)
         scales = x.new_empty(T, H // 128, dtype=_F32)
@@ -133,7 +137,7 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False
     if rstd:
         rs = x.new_empty(T, dtype=_F32)
         rp = rs.data_ptr()
-    _check(lib().moe_rms_norm(x.data_ptr(), r, w, T, H, eps, yp, sp, cp, kp, rp, _raw_stream(dev)), "moe_rms_norm")
+    _check(lib().moe_rms_norm(xp, r, w, T, H, eps, yp, sp, cp, kp, rp, _raw_stream(dev)), "moe_rms_norm")
     return RMSNormOutput(y, s, codes, scales, rs)
 
 

@@ -65,3 +65,22 @@ def test_stream_without_a_residual_in_place(T, H):
     a, s = x.clone(), torch.full_like(x, 7.0)
     c_norm(a, None, w, a, s)
     assert torch.equal(s, x) and torch.equal(a, want)
+
+
+def test_stream_is_not_claimed_where_y_took_its_place():
+    """Without a residual the stream is x itself; in place it is gone, so none is handed on."""
+    x, w = normal(1, 6, 64), normal(2, 64, mean=1.0)
+    want = moe.rms_norm(x, w, rstd=True)
+    assert want.residual is x
+    for name in (lambda t: t, lambda t: t.view(6, 64)):  # the same memory by either name
+        a = x.clone()
+        got = moe.rms_norm(a, w, rstd=True, out=name(a))
+        assert torch.equal(got.y, want.y) and torch.equal(got.rstd, want.rstd)
+        assert got.residual is None
+        with pytest.raises(TypeError, match="s must be"):
+            moe.rms_norm_backward(x, got.residual, w, got.rstd)
+    a, r = x.clone(), normal(3, 6, 64)
+    got = moe.rms_norm(a, w, residual=r, out=a)  # with a residual the stream has a buffer of its own
+    assert torch.equal(got.residual.double(), R.norm(x, w, r, 1e-6)[0])
+    none = x[:0]
+    assert moe.rms_norm(none, w).residual is none and moe.rms_norm(none, w, out=none).residual is none
