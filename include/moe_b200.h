@@ -237,7 +237,9 @@ moe_status moe_read_device_status(const void* workspace, void* stream);
  *    loads, so the MMA issuer waits on a barrier nothing completes and gives up
  *    after wait_limit_ns (on the FUSED path the gate/up tasks count no
  *    completions, so the down tasks' waits give up); the rest of the call then
- *    runs on stale intermediates and its output is garbage. 0 turns it off.
+ *    runs on stale intermediates and its output is garbage. 0 turns it off. In
+ *    the dense operators' GEMMs the last CTA of each cluster issues no loads, so
+ *    that its own waits give up and its peers' on what it owes them.
  *
  * Both are process-wide and read when a call is enqueued; do not change them
  * while other threads enqueue calls. Returns MOE_ERR_INVALID_ARG (and changes

@@ -352,8 +352,8 @@ def router(x: torch.Tensor, w_router: torch.Tensor, k: int, logits: bool = False
 
 def set_test_hooks(stall_gate_up_loads: bool = False, wait_limit_ns: int = 0) -> None:
     """Failure-detection test switches (moe_set_test_hooks): the limit of every
-    bounded device wait (0 = the 2 s default) and a stall of the prefill
-    gate/up GEMM's loads. Raises MoeError on values out of range."""
+    bounded device wait (0 = the 2 s default) and a stall of the loads of the
+    prefill gate/up GEMM and of the dense operators' GEMMs. Raises MoeError on values out of range."""
     _check(lib().moe_set_test_hooks(int(bool(stall_gate_up_loads)), int(wait_limit_ns)), "moe_set_test_hooks")
 
 

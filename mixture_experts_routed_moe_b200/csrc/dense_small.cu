@@ -21,7 +21,8 @@
 // distributed shared memory between two cluster barriers, 1.9 so).
 //
 // Warps: 0 TMA producer, 1 MMA issuer; then all send and add. Every wait
-// is bounded; a cluster with a wait that gave up writes NaN.
+// is bounded; a cluster with a wait that gave up writes NaN, and none of its CTAs that
+// gave up ends before the others have stopped sending.
 #include <algorithm>
 #include <limits>
 #include <type_traits>
@@ -46,7 +47,7 @@ struct SmallParams {
   uint32_t n_alloc;  // TMEM columns (power of two >= 32)
   int stages;        // of the ring, kA + n_pad * 128 bytes each
   int rows;          // outputs of a unit, a multiple of 8
-  int act, stall;
+  int act, stall;    // stall (failure tests): the last CTA of a cluster issues no loads
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
   __nv_bfloat16* out;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kManyThreads)
   pdl_trigger();
 
   if (warp == 0) {
-    if (!p.stall) {
+    if (!p.stall || rank + 1 < csize) {
       const bool one = elect_one();
       int stage = 0;
       uint32_t ph = 0;
@@ -360,7 +361,15 @@ __global__ void __launch_bounds__(kManyThreads)
     default:
       end(std::integral_constant<int, 8>{});
   }
-  __syncthreads();
+  if (__syncthreads_or(aborted)) {
+    // This CTA gave up on partials that a slower peer may still send into it. It stays until
+    // every peer has come here too or has ended (threads that have do not count in the
+    // barrier, so that the others pass by it), and then for what was sent last to land.
+    cluster_arrive();
+    cluster_wait();
+    if (threadIdx.x == 0) mbar_wait_bounded(arrived, 0, &never, s_status, 1000000ull);
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, p.n_alloc);

@@ -1,0 +1,51 @@
+"""Waits of the dense GEMMs that give up, without a fault: one CTA of each cluster issues
+no loads, so that its own waits and its peers' run into a short limit. Each call returns
+with NaN in what it did not compute, and the next one gives the right bits."""
+import time
+
+import pytest
+import torch
+
+import mixture_experts_routed_moe_b200 as moe
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+LIMIT_NS = 20_000_000  # 20 ms
+
+
+def normal(seed, *shape, std=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").mul_(std).to(BF)
+
+
+def stalled(f):
+    """f() with the loads withheld, and the seconds it took."""
+    torch.cuda.synchronize()
+    try:
+        moe.set_test_hooks(stall_gate_up_loads=True, wait_limit_ns=LIMIT_NS)
+        t = time.perf_counter()
+        out = f()
+        torch.cuda.synchronize()
+        return out, time.perf_counter() - t
+    finally:
+        moe.set_test_hooks()
+
+
+# clusters of eight, four, two and one; one token tile and several; whole and half SMs
+SPLIT = [(40, 7168, 136), (33, 2048, 1408), (64, 2048, 7168), (100, 512, 4096), (333, 2040, 1000), (40, 64, 264)]
+
+
+@pytest.mark.parametrize("T,K,N", SPLIT)
+@pytest.mark.parametrize("op", ["linear", "gated", "dx"])
+def test_a_cluster_whose_partials_never_come(T, K, N, op):
+    x, w = normal(1, T, K), normal(2, 2 * N if op == "gated" else N, K, std=K ** -0.5)
+    d = normal(3, T, N)
+    call = {"linear": lambda: moe.linear(x, w), "gated": lambda: moe.gated_ffn(x, w),
+            "dx": lambda: moe.linear_backward(d, x, w)[0]}[op]
+    want = call()
+    for _ in range(2):
+        got, seconds = stalled(call)
+        assert torch.isnan(got).all()
+        assert seconds < 1.0  # the short limit ended the waits
+        assert torch.equal(call(), want)
