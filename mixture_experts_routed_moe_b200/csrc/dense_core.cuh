@@ -28,6 +28,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, status, limit_ns));
 }
 
+// After a wait that gave up: the loads that the producer had issued when it stopped at
+// (stage, phase) land in the ring, or a millisecond a stage passes.
+__device__ __forceinline__ void drain_loads(uint64_t* full, int stages, int stage, uint32_t phase, int* status) {
+  for (int i = 0; i < stages; ++i) {
+    if (--stage < 0) {
+      stage = stages - 1;
+      phase ^= 1;
+    }
+    int never = 0;
+    mbar_wait_bounded(&full[stage], phase, &never, status, 1000000ull);
+  }
+}
+
 // The two halves of cluster_sync.
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");

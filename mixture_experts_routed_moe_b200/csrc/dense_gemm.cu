@@ -67,7 +67,7 @@ struct Product {
 struct GemmParams {
   Product prod[2];  // the second only in backward mode
   int first_tiles, full, tiles;  // tiles of the first product; whole tiles of both; with the half ones
-  int act, save, stall;
+  int act, save, stall;  // stall (failure tests): the last CTA of a tile issues no loads
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
   unsigned long long timeout_ns;
@@ -231,8 +231,10 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
   const int total = p.tiles;
   const int worker = blockIdx.x / TL::kCtas, nworkers = gridDim.x / TL::kCtas;
 
+  int next = 0;  // where the producer stops: the ring's next stage, its phase
+  uint32_t next_ph = 0;
   if (warp == 0) {
-    if (!p.stall) {
+    if (!p.stall || rank + 1 < TL::kCtas) {
       // ---------------- TMA producer ----------------
       const bool one = elect_one();
       int stage = 0;
@@ -292,17 +294,8 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
           }
         }
       }
-      if (!ok && leader && one) {
-        // let the copies already issued (of both CTAs) land before the CTA can exit
-        for (int i = 0; i < kStages; ++i) {
-          if (--stage < 0) {
-            stage = kStages - 1;
-            ph ^= 1;
-          }
-          int never = 0;
-          mbar_wait_bounded(&full[stage], ph, &never, s_status, 1000000ull);
-        }
-      }
+      next = stage;
+      next_ph = ph;
     }
   } else if (warp == 1) {
     if (leader) {
@@ -484,7 +477,7 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
 
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(*s_abort) != 0;
   if (kPair) cluster_sync();  // neither CTA frees TMEM while the pair still uses it
   if (warp == 1) {
     tc_fence_after();
@@ -492,6 +485,16 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
       tmem_dealloc_pair(tmem_base, 2 * kBN);
     else
       tmem_dealloc(tmem_base, 2 * kBN);
+  }
+  if (gave_up) {
+    // A wait gave up (never in normal operation), perhaps in a role that waited for loads
+    // after the producer had issued its last: no load is issued any more, and those on
+    // their way land before the shared memory is given back. In a pair they are counted in
+    // the leader. A CTA that did not give up has seen all of both CTAs' loads and may have
+    // ended (threads that have do not count in the barrier).
+    if (leader && threadIdx.x == 0) drain_loads(full, kStages, next, next_ph, s_status);
+    __syncwarp();
+    if (kPair) cluster_sync();
   }
 }
 

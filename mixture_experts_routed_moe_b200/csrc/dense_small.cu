@@ -231,13 +231,14 @@ __global__ void __launch_bounds__(kManyThreads)
   pdl_wait();  // the previous kernel on the stream has completed; its writes are visible
   pdl_trigger();
 
+  int next = 0;  // where the producer stops: the ring's next stage, its phase
+  uint32_t next_ph = 0;
   if (warp == 0) {
     if (!p.stall || rank + 1 < csize) {
       const bool one = elect_one();
       int stage = 0;
       uint32_t ph = 0;
-      int kb = kb0;
-      for (; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!warp_wait(&empty[stage], ph ^ 1, s_abort, s_status, p.timeout_ns)) break;
         if (one) {
           mbar_arrive_expect_tx(&full[stage], stage_bytes);
@@ -260,17 +261,8 @@ __global__ void __launch_bounds__(kManyThreads)
           ph ^= 1;
         }
       }
-      if (kb < kb1 && one) {
-        // let the copies already issued land before the shared memory is reused
-        for (int i = 0; i < kStages; ++i) {
-          if (--stage < 0) {
-            stage = kStages - 1;
-            ph ^= 1;
-          }
-          int never = 0;
-          mbar_wait_bounded(&full[stage], ph, &never, s_status, 1000000ull);
-        }
-      }
+      next = stage;
+      next_ph = ph;
     }
   } else if (warp == 1) {
     const bool one = elect_one();
@@ -295,12 +287,7 @@ __global__ void __launch_bounds__(kManyThreads)
         ph ^= 1;
       }
     }
-    if (one) {
-      umma_commit(tfull);
-      // MMAs in flight end before the tensor memory is freed, also after a wait that gave up
-      int never = 0;
-      if (*s_abort) mbar_wait_bounded(tfull, 0, &never, s_status, 1000000ull);
-    }
+    if (one) umma_commit(tfull);
     __syncwarp();
   }
   // All warps send the partial: two or four per TMEM lane quadrant, taking the blocks
@@ -361,10 +348,17 @@ __global__ void __launch_bounds__(kManyThreads)
     default:
       end(std::integral_constant<int, 8>{});
   }
-  if (__syncthreads_or(aborted)) {
-    // This CTA gave up on partials that a slower peer may still send into it. It stays until
-    // every peer has come here too or has ended (threads that have do not count in the
-    // barrier, so that the others pass by it), and then for what was sent last to land.
+  if (__syncthreads_or(aborted || *s_abort)) {
+    // A wait gave up (never in normal operation), here or in another role, after the loads
+    // and MMAs that it waited for or stopped were issued: they end before the shared and
+    // the tensor memory are given back.
+    never = 0;
+    if (threadIdx.x == 0) drain_loads(full, kStages, next, next_ph, s_status);
+    if (threadIdx.x == 32) mbar_wait_bounded(tfull, 0, &never, s_status, 1000000ull);
+    __syncthreads();
+    // Slower peers may still send partials into this CTA. It stays until every peer has come
+    // here too or has ended (threads that have do not count in the barrier, so that the
+    // others pass by it), and then for what was sent last to land.
     cluster_arrive();
     cluster_wait();
     if (threadIdx.x == 0) mbar_wait_bounded(arrived, 0, &never, s_status, 1000000ull);

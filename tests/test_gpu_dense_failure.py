@@ -49,3 +49,23 @@ def test_a_cluster_whose_partials_never_come(T, K, N, op):
         assert torch.isnan(got).all()
         assert seconds < 1.0  # the short limit ended the waits
         assert torch.equal(call(), want)
+
+
+# tiles of CTA pairs, of which the leader's loads are on their way when it gives up, and of
+# single CTAs; fewer K steps than the ring has stages, so that the producer is done by then, and more
+TILES = [(4096, 2048, 1408), (4096, 136, 2048), (1000, 520, 2056), (700, 64, 520), (2050, 2048, 4104)]
+
+
+@pytest.mark.parametrize("T,K,N", TILES)
+@pytest.mark.parametrize("op", ["linear", "gated", "backward"])
+def test_tiles_whose_loads_never_come(T, K, N, op):
+    x, w = normal(1, T, K), normal(2, 2 * N if op == "gated" else N, K, std=K ** -0.5)
+    d = normal(3, T, N)
+    call = {"linear": lambda: [moe.linear(x, w, residual=d)], "gated": lambda: [moe.gated_ffn(x, w)],
+            "backward": lambda: list(moe.linear_backward(d, x, w)[:2])}[op]
+    want = call()
+    for _ in range(2):
+        got, seconds = stalled(call)
+        assert all(bool(torch.isnan(t).all()) for t in got)
+        assert seconds < 1.0
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
