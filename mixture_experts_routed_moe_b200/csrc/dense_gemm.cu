@@ -67,7 +67,8 @@ struct Product {
 struct GemmParams {
   Product prod[2];  // the second only in backward mode
   int first_tiles, full, tiles;  // tiles of the first product; whole tiles of both; with the half ones
-  int act, save, stall;  // stall (failure tests): the last CTA of a tile issues no loads
+  int act, stall;                // stall (failure tests): the last CTA of a tile issues no loads
+  void* save;                    // linear: bf16 z [M, N]; gated: fp32 [M, 2N]; or null
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
   unsigned long long timeout_ns;
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
           float u[32];
           tmem_load32(tb + c, v);
           tmem_load32(tb + outn + c, u);
-          if (p.save) {
+          if (p.save != nullptr) {
             st.store_f32(&maps.save[0], v, x, y0, N, rows);
             st.store_f32(&maps.save[1], u, x, y0, N, rows);
           }
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
               }
             }
           }
-          if (p.save) st.store_bf16(&maps.save[0], v, x, y0, rows && x < N);
+          if (p.save != nullptr) st.store_bf16(&maps.save[0], v, x, y0, rows && x < N);
           if (p.act != kActNone) {
             with_act(p.act, [&](auto tag) {
 #pragma unroll
@@ -469,10 +470,20 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
       const int outn = kGated ? co.nb / 2 : co.nb;
       const Product& pr = p.prod[co.prob];
       const int y = (co.m * TL::kCtas + rank) * kTileM + quad * 32 + lane;
-      if (y < pr.M)
-        for (int c = 32 * part; c < outn; c += 32 * kParts)
-          for (int x = co.x + c; x < min(co.x + c + 32, pr.N); ++x)
-            pr.out[static_cast<size_t>(y) * pr.N + x] = __ushort_as_bfloat16(0x7FC0);
+      if (y >= pr.M) continue;
+      const __nv_bfloat16 nan = __ushort_as_bfloat16(0x7FC0);
+      for (int c = 32 * part; c < outn; c += 32 * kParts)
+        for (int x = co.x + c; x < min(co.x + c + 32, pr.N); ++x) {
+          const size_t at = static_cast<size_t>(y) * pr.N + x;
+          pr.out[at] = nan;
+          if (kMode == kModeBackward || p.save == nullptr) continue;
+          if (kGated) {
+            float* gu = static_cast<float*>(p.save) + static_cast<size_t>(y) * pr.N + at;
+            gu[0] = gu[pr.N] = __bfloat162float(nan);
+          } else {
+            static_cast<__nv_bfloat16*>(p.save)[at] = nan;
+          }
+        }
     }
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
@@ -542,13 +553,13 @@ cudaError_t launch_t(const DenseGemm* g, int n, int num_sms, cudaStream_t st) {
     maps.y[1] = maps.y[0];
   }
   p.act = g->act;
-  p.save = g->save != nullptr;
+  p.save = g->save;
   p.stall = stall_gate_up_loads();
   p.bias = static_cast<const __nv_bfloat16*>(g->bias);
   p.residual = static_cast<const __nv_bfloat16*>(g->residual);
   p.timeout_ns = wait_limit_ns();
   maps.save[0] = maps.save[1] = maps.y[0];
-  if (p.save) {
+  if (p.save != nullptr) {
     for (int i = 0; i < (kGated ? 2 : 1); ++i) {
       const bool encoded =
           kGated ? encode_tensor_map_2d_ld(&maps.save[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,

@@ -70,7 +70,7 @@ int ring_stages(int tile_t, int n_pad) {
 // residual, the one rounding. `res` and `bias` are the four values' inputs.
 template <bool kGated>
 __device__ __forceinline__ void write_outputs(const SmallParams& p, float4 z, float4 u, uint2 bias, uint2 res, int t,
-                                              int n, bool aborted) {
+                                              int n) {
   const size_t at = static_cast<size_t>(t) * p.N + n;
   float v[4];
   if (!kGated && p.bias != nullptr) {
@@ -109,9 +109,7 @@ __device__ __forceinline__ void write_outputs(const SmallParams& p, float4 z, fl
     v[2] += bf16_lo(res.y);
     v[3] += bf16_hi(res.y);
   }
-  uint2 o = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-  if (aborted) o = make_uint2(0x7FC07FC0u, 0x7FC07FC0u);
-  *reinterpret_cast<uint2*>(p.out + at) = o;
+  *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 // The bias and the residual of four outputs.
@@ -154,7 +152,11 @@ __device__ __forceinline__ void finish(const SmallParams& p, const float* s_part
         u[0].w += u[q].w;
       }
     }
-    write_outputs<kGated>(p, g[0], u[0], bi, re, t0 + t, n, aborted);
+    if (aborted) {  // sums that never came: NaN in what is kept, and so in the output
+      const float nan = __int_as_float(0x7FC00000);
+      g[0] = u[0] = make_float4(nan, nan, nan, nan);
+    }
+    write_outputs<kGated>(p, g[0], u[0], bi, re, t0 + t, n);
   };
   for (int i = threadIdx.x; i < nt * per; i += blockDim.x) {
     const uint2 bi = bias[0], re = res[0];
@@ -348,10 +350,10 @@ __global__ void __launch_bounds__(kManyThreads)
     default:
       end(std::integral_constant<int, 8>{});
   }
-  if (__syncthreads_or(aborted || *s_abort)) {
-    // A wait gave up (never in normal operation), here or in another role, after the loads
-    // and MMAs that it waited for or stopped were issued: they end before the shared and
-    // the tensor memory are given back.
+  if (__syncthreads_or(aborted)) {
+    // A wait gave up (never in normal operation), here or in a role whose part of this CTA's
+    // partial then went to nobody, after the loads and MMAs that it waited for or stopped
+    // were issued: they end before the shared and the tensor memory are given back.
     never = 0;
     if (threadIdx.x == 0) drain_loads(full, kStages, next, next_ph, s_status);
     if (threadIdx.x == 32) mbar_wait_bounded(tfull, 0, &never, s_status, 1000000ull);

@@ -69,3 +69,26 @@ def test_tiles_whose_loads_never_come(T, K, N, op):
         assert all(bool(torch.isnan(t).all()) for t in got)
         assert seconds < 1.0
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+@pytest.mark.parametrize("T,H,I", [(40, 512, 264), (333, 2040, 1000), (700, 64, 520), (4096, 136, 2048)])
+@pytest.mark.parametrize("name", ["silu", "gelu", "relu"])
+def test_kept_pre_activations_are_marked_too(T, H, I, name):
+    """Through the C entry points, into buffers that held finite numbers: with the output, g
+    and u and z are NaN, so that no gradient is formed of what was never computed."""
+    x, wg, wd = normal(1, T, H), normal(2, 2 * I, H, std=H ** -0.5), normal(3, I, H, std=H ** -0.5)
+    h, y, z = (torch.ones((T, I), device="cuda", dtype=BF) for _ in range(3))
+    gu = torch.ones((T, 2 * I), device="cuda")
+    L, act, st = moe.lib(), moe.ACT[name], torch.cuda.current_stream().cuda_stream
+
+    def both():
+        assert L.moe_gated_ffn(x.data_ptr(), wg.data_ptr(), T, H, I, act, h.data_ptr(), gu.data_ptr(), st) == 0
+        assert L.moe_linear(x.data_ptr(), wd.data_ptr(), None, None, T, H, I, act, y.data_ptr(), z.data_ptr(), st) == 0
+
+    both()
+    want = [t.clone() for t in (h, gu, y, z)]
+    stalled(both)
+    for t in (h, gu, y, z):
+        assert torch.isnan(t).all()
+    both()
+    assert all(torch.equal(a, b) for a, b in zip((h, gu, y, z), want))
