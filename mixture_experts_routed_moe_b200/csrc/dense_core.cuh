@@ -190,22 +190,23 @@ __device__ __forceinline__ void act_and_slope2(const float (&z)[2], float (&f)[2
   }
 }
 
-// Runs f with the activation as a compile-time constant.
+// Runs f with the activation as a compile-time constant; a gate always has one (kNone false).
 template <int kAct>
 struct ActTag {
   static constexpr int value = kAct;
 };
-template <typename F>
+template <bool kNone, typename F>
 __host__ __device__ __forceinline__ auto with_act(int act, F&& f) {
   switch (act) {
     case MOE_ACT_SILU:
       return f(ActTag<MOE_ACT_SILU>{});
     case MOE_ACT_GELU:
       return f(ActTag<MOE_ACT_GELU>{});
-    case MOE_ACT_RELU:
-      return f(ActTag<MOE_ACT_RELU>{});
     default:
-      return f(ActTag<kActNone>{});
+      if constexpr (kNone) {
+        if (act == kActNone) return f(ActTag<kActNone>{});
+      }
+      return f(ActTag<MOE_ACT_RELU>{});
   }
 }
 

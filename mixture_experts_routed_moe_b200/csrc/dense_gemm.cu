@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
             st.store_f32(&maps.save[0], v, x, y0, N, rows);
             st.store_f32(&maps.save[1], u, x, y0, N, rows);
           }
-          with_act(p.act, [&](auto tag) {
+          with_act<false>(p.act, [&](auto tag) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               act2<decltype(tag)::value>(v[i], v[i + 1]);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Epilogue<kMode>::kThreads, 1)
           }
           if (p.save != nullptr) st.store_bf16(&maps.save[0], v, x, y0, rows && x < N);
           if (p.act != kActNone) {
-            with_act(p.act, [&](auto tag) {
+            with_act<false>(p.act, [&](auto tag) {
 #pragma unroll
               for (int i = 0; i < 32; i += 2) act2<decltype(tag)::value>(v[i], v[i + 1]);
             });

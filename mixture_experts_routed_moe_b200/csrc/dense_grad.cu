@@ -123,7 +123,7 @@ cudaError_t launch_gated_grad(const float* gu, const void* dh, void* dgu, int T,
   const long long n = static_cast<long long>(T) * (I / 8);
   // a thread a vector (4096 x 14336: 117 us; one wave of blocks that walk 126)
   const long long blocks = std::min<long long>((n + 255) / 256, static_cast<long long>(num_sms) * 256);
-  return with_act(act, [&](auto tag) {
+  return with_act<false>(act, [&](auto tag) {
     return launch_pdl(gated_grad_kernel<decltype(tag)::value>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
                       gu, static_cast<const __nv_bfloat16*>(dh), static_cast<__nv_bfloat16*>(dgu),
                       static_cast<long long>(T), I);
@@ -140,7 +140,7 @@ cudaError_t launch_linear_grad(const void* z, const void* dy, void* dz, float* p
                                int act, cudaStream_t st) {
   const int rows = linear_grad_rows(T, N);
   const dim3 grid(static_cast<unsigned>((N + kGradCols - 1) / kGradCols), static_cast<unsigned>(rows));
-  const cudaError_t err = with_act(act, [&](auto tag) {
+  const cudaError_t err = with_act<true>(act, [&](auto tag) {
     return launch_pdl(linear_grad_kernel<decltype(tag)::value>, grid, dim3(256), 0, st,
                       static_cast<const __nv_bfloat16*>(z),
                       static_cast<const __nv_bfloat16*>(dy), static_cast<__nv_bfloat16*>(dz),

@@ -89,7 +89,7 @@ __device__ __forceinline__ void write_outputs(const SmallParams& p, float4 z, fl
           make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
     }
   }
-  with_act(p.act, [&](auto tag) {
+  with_act<!kGated>(p.act, [&](auto tag) {
     constexpr int kAct = decltype(tag)::value;
     act2<kAct>(z.x, z.y);
     act2<kAct>(z.z, z.w);

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) dense_vec_kernel(const VecP
         gu[p.N] = z[2 + i];
       }
     }
-    with_act(p.act, [&](auto tag) { act2<decltype(tag)::value>(z[0], z[1]); });
+    with_act<false>(p.act, [&](auto tag) { act2<decltype(tag)::value>(z[0], z[1]); });
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (t0 + i < p.T) p.out[static_cast<size_t>(t0 + i) * p.N + n] = __float2bfloat16_rn(z[i] * z[2 + i]);
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) dense_vec_kernel(const VecP
       for (int i = 0; i < 2; ++i)
         if (p.save != nullptr && t0 + i < p.T)
           static_cast<__nv_bfloat16*>(p.save)[o + i * static_cast<size_t>(p.N)] = __float2bfloat16_rn(y[i]);
-      with_act(p.act, [&](auto tag) { act2<decltype(tag)::value>(y[0], y[1]); });
+      with_act<true>(p.act, [&](auto tag) { act2<decltype(tag)::value>(y[0], y[1]); });
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (t0 + i >= p.T) continue;
