@@ -401,7 +401,8 @@ class MoEBlock:
 
     ``block(x, residual)`` returns (y, s), both bf16 [T,H]: the next norm's x and
     residual. e4m3 experts take the norm's codes and scales. Calls share the
-    layer's workspace: order them, for example on one stream."""
+    layer's workspace: order them, for example on one stream. For inference: the
+    router and the routed experts have no backward pass, and nothing is kept for one."""
 
     def __init__(self, layer: "MoELayer", w_norm, w_router, shared_gate_up=None, shared_down=None,
                  eps: float = 1e-6):

@@ -1,6 +1,6 @@
 // Elementwise halves of the dense operators' backward passes: the gradients
 // at the pre-activations, from the pre-activations the forward kept (g and u in
-// fp32, z in bf16).
+// fp32, z in bf16: what that costs the slope stands at dense_gemm.cu's head).
 //
 //   gated:  dg = dh u act'(g),  du = dh act(g)        -> bf16 [T, 2I]
 //   linear: dz = dy act'(z)                           -> bf16 [T, N]

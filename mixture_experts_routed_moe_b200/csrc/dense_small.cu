@@ -378,9 +378,9 @@ struct Plan {
   double us;  // estimated time; infinite where the CTAs would not be resident together
 };
 
-// Sixteen warps where a CTA sends and adds a large partial (linear 2048 -> 7168 for 200
-// tokens 21.4 us with eight, 17.6 with sixteen, for 96 13.6 and 11.8); with small ones and
-// with the gated epilogue they cost up to 8%.
+// Sixteen warps where a CTA sends and adds a large partial (linear with a residual 2048 ->
+// 7168 for 96 tokens 13.4 us with eight, 11.5 with sixteen, 4096 -> 4096 for 256 20.4 and
+// 17.9); with small ones and with the gated epilogue they cost up to 8%.
 int threads_of(const DenseGemm& g, int tile_t, int rows, int csize) {
   return g.order != kGatedNT && tile_t * rows / csize >= 6000 ? kManyThreads : kThreads;
 }

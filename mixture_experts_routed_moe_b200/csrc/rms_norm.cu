@@ -9,7 +9,10 @@
 //   dw_i = sum_t dy_i s_i r
 //
 // Bound by HBM: every element is read once and written once, the row stays in
-// registers between the sum of squares and the scaling. The sum of squares,
+// registers between the sum of squares and the scaling. (Beyond 16384 columns a thread
+// holds eight vectors, more than its 64 registers take: 0.7 to 1.5 KB a thread are spilled,
+// and 4096 x 32768 with a residual takes 591 us = 1.8 TB/s, its backward pass 559; 4096 x
+// 16384 91 and 166 us.) The sum of squares,
 // r, the scaling and all gradient sums are fp32; s is rounded to bf16 because
 // that is the value the residual stream keeps (and the backward pass reads),
 // y, dx and dw are rounded once at the end, the codes straight from fp32.
@@ -496,16 +499,17 @@ cudaError_t launch_rms_norm(const void* x, const void* residual, const void* wei
 
 namespace {
 
-// Threads that share a row of the backward pass, and rows of a block at a time:
-// blocks of 256 threads and more.
+// Threads that share a row of the backward pass, and rows of a block at a time: as many as
+// fit into 256 threads, or one (blocks of 160 to 512 threads with one vector a thread).
 int backward_vec(int nvec) { return nvec <= 512 ? 1 : nvec <= 1024 ? 2 : nvec <= 2048 ? 4 : 8; }
 int backward_tpr(int nvec) { return round32((nvec + backward_vec(nvec) - 1) / backward_vec(nvec)); }
 int backward_groups(int nvec) { return std::max(1, 256 / backward_tpr(nvec)); }
 
 }  // namespace
 
-// Partial rows of the weight gradient: the blocks that are resident at once, 1024
-// threads an SM with one vector a thread, else one block (its registers fill the
+// Partial rows of the weight gradient: the blocks that run at once, with one vector a
+// thread as many as 1024 threads an SM allow and at most four (640 to 1024 threads, by the
+// width; 8192 x 768 15.5 us, x 1280 21.9, x 2048 26.6), else one block (its registers fill the
 // SM; two blocks an SM leave twice the partial rows: 4096 x 7168 46.6 us against 44.4).
 int rms_norm_backward_blocks(int T, int H) {
   const int nvec = H / 8, groups = backward_groups(nvec), block = groups * backward_tpr(nvec);

@@ -5,9 +5,17 @@ projection with bias, activation and residual, each with its backward pass.
 Thin bindings over the C ABI (``moe_rms_norm``, ``moe_gated_ffn``,
 ``moe_linear`` and their ``_backward`` forms): they check the tensors, allocate
 outputs and workspaces that the caller did not pass, and launch on the current
-stream (or ``stream``). All tensors are contiguous and share one CUDA device;
-activations, weights and gradients are bfloat16. Nothing synchronises, and
-every call can be captured in a CUDA graph after one eager call.
+stream. All tensors are contiguous and share one CUDA device; activations,
+weights and gradients are bfloat16. Nothing synchronises, and every call can be
+captured in a CUDA graph after one eager call.
+
+``stream`` takes a call to another stream, its new outputs and workspaces
+included. It does not wait there for whoever wrote the inputs, nor keep them
+alive: order that stream behind the writer's (``stream.wait_stream``), and hold
+inputs, or call their ``record_stream``, until its work is done.
+
+Gradients are explicit calls, not autograd's: a result carries no graph, also
+where an input requires grad, and ``backward()`` does not reach what came before.
 """
 from __future__ import annotations
 
